@@ -8,6 +8,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -35,6 +36,8 @@ MOE_FLAG_FFN_PAIRS = 1 << 8
 MOE_FLAG_FFN_SINGLE = 1 << 9
 MOE_FLAG_FFN_ROWS_COPY = 1 << 10
 MOE_FLAG_FFN_ROWS_GATHER = 1 << 11
+MOE_FLAG_W4_ZEROS = 1 << 12
+MOE_FLAG_F32_OUT = 1 << 13
 MOE_COMBINE_F32 = 1 << 0
 
 _ROUTER_FLAGS = {"auto": 0, "fp64": MOE_FLAG_ROUTER_FP64, "screen": MOE_FLAG_ROUTER_SCREEN}
@@ -74,6 +77,16 @@ SIGNATURES = {
     "moe_nvfp4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _U]),
     "moe_forward_nvfp4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _U, ctypes.c_float,
                                ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "moe_w4_packed_bytes": (_SZ, [_I, _I, _I, _I, _U]),
+    "moe_w4_pack": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_w4_quantize_weights": (_I, [_P, _I, _I, _I, _I, _U, _P, _P]),
+    "moe_w4_dequantize_weights": (_I, [_P, _I, _I, _I, _I, _U, _P, _P]),
+    "moe_linear_w4": (_I, [_P, _P, _I, _I, _I, _I, _U, _P, _P]),
+    "moe_dense_w4_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_dense_ffn_w4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _U, _P, _P, _SZ, _P]),
+    "moe_w4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _U]),
+    "moe_forward_w4": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _U, _P, _P, _P, _SZ,
+                            _P]),
     "moe_sync_status": (_I, [_P]),
     "moe_ffn_kernel_name": (ctypes.c_char_p, [_I, _U]),
     "moe_last_stage_times": (_I, [ctypes.POINTER(ctypes.c_float), _I]),
@@ -455,6 +468,254 @@ def forward_nvfp4(x: torch.Tensor, w_router: torch.Tensor, wq: dict, k: int,
                                None if a is None else ctypes.byref(a), ws.data_ptr(), ws.numel(),
                                _stream_ptr(stream)), "moe_forward_nvfp4")
     return (y, aux_d) if aux else y
+
+
+# ----------------------------------------------------------------------------- 4-bit weights
+class W4Weights:
+    """E matrices [K, N] as packed 4-bit codes with group scales (and zero points): the layout of
+    include/moe.h in ``data`` (uint8 [E, N/16, K/64, R], CUDA).  Made by w4_pack or w4_quantize."""
+
+    __slots__ = ("data", "E", "K", "N", "group", "zeros", "flags")
+
+    def __init__(self, data: torch.Tensor, E: int, K: int, N: int, group: int, zeros: bool):
+        self.data, self.E, self.K, self.N, self.group, self.zeros = data, E, K, N, group, zeros
+        self.flags = MOE_FLAG_W4_ZEROS if zeros else 0
+
+    @property
+    def shape(self) -> tuple[int, int, int]:
+        return (self.E, self.K, self.N)
+
+    @property
+    def device(self) -> torch.device:
+        return self.data.device
+
+    def __repr__(self) -> str:
+        return (f"W4Weights(E={self.E}, K={self.K}, N={self.N}, group={self.group}, "
+                f"zeros={self.zeros}, device={self.device})")
+
+
+def _on_device(fn):
+    """Run a call on its first argument's device and on `stream` (default: that device's current
+    one), so that memory the call allocates belongs to the stream that its kernels run on."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        t = first.data if isinstance(first, W4Weights) else first
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("the first argument must be a CUDA tensor or W4Weights")
+        if stream is None and t.device.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(t.device):
+            with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+                if torch.cuda.current_device() != t.device.index:
+                    raise ValueError("stream belongs to another device than the tensors")
+                return fn(first, *args, **kw)
+    return call
+
+
+def _same(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> int:
+    p = _dev(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return p
+
+
+def _w4(w: W4Weights, name: str, E: int, K: int, N: int, dev: torch.device) -> int:
+    if not isinstance(w, W4Weights):
+        raise TypeError(f"{name} must be W4Weights (w4_pack, w4_quantize)")
+    if w.E != E or w.K != K or w.N != N:
+        raise ValueError(f"{name} must hold {E} matrices of [{K}, {N}], got {w}")
+    if w.data.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {w.data.device}")
+    return w.data.data_ptr()
+
+
+def _w4_empty(E: int, K: int, N: int, group: int, zeros: bool, dev) -> W4Weights:
+    n = load().moe_w4_packed_bytes(E, K, N, group, MOE_FLAG_W4_ZEROS if zeros else 0)
+    if n == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED if group in (32, 64, 128) else MOE_ERR_INVALID_ARG,
+                       "moe_w4_packed_bytes")
+    data = torch.empty((E, N // 16, K // 64, n // (E * (N // 16) * (K // 64))), dtype=torch.uint8,
+                       device=dev)
+    return W4Weights(data, E, K, N, group, zeros)
+
+
+def _raw_stream(dev: torch.device) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+@_on_device
+def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
+            group: int = 64) -> W4Weights:
+    """moe_w4_pack: a checkpoint's 4-bit matrices -> W4Weights.  codes uint8 [E, N, K/2] (element
+    2b in the low nibble of byte b), scales bf16 [E, N, ceil(K/group)], zeros uint8 of the same
+    shape or None (symmetric, zero point 8); one matrix may leave E out."""
+    if codes.dim() == 2:
+        codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
+        zeros = None if zeros is None else zeros.unsqueeze(0)
+    if codes.dim() != 3:
+        raise ValueError(f"codes must be [E, N, K/2] or [N, K/2], got {tuple(codes.shape)}")
+    E, N, half = codes.shape
+    K, dev = 2 * half, codes.device
+    w = _w4_empty(E, K, N, group, zeros is not None, dev)
+    G = -(-K // group)
+    pc = _same(codes, "codes", torch.uint8, (E, N, half), dev)
+    ps = _same(scales, "scales", torch.bfloat16, (E, N, G), dev)
+    pz = None if zeros is None else _same(zeros, "zeros", torch.uint8, (E, N, G), dev)
+    _check(load().moe_w4_pack(pc, ps, pz, E, K, N, group, w.data.data_ptr(), _raw_stream(dev)),
+           "moe_w4_pack")
+    return w
+
+
+@_on_device
+def w4_quantize(w: torch.Tensor, group: int = 64, zeros: bool = False) -> W4Weights:
+    """moe_w4_quantize_weights: bf16 w [E, K, N] or [K, N] (N contiguous) -> W4Weights, symmetric
+    or (zeros=True) with a zero point per group."""
+    if w.dim() == 2:
+        w = w.unsqueeze(0)
+    if w.dim() != 3:
+        raise ValueError(f"w must be [E, K, N] or [K, N], got {tuple(w.shape)}")
+    E, K, N = w.shape
+    dev = w.device
+    pw = _same(w, "w", torch.bfloat16, (E, K, N), dev)
+    q = _w4_empty(E, K, N, group, zeros, dev)
+    _check(load().moe_w4_quantize_weights(pw, E, K, N, group, q.flags, q.data.data_ptr(),
+                                          _raw_stream(dev)), "moe_w4_quantize_weights")
+    return q
+
+
+@_on_device
+def w4_dequantize(w: W4Weights, out: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_w4_dequantize_weights: the bf16 weights [E, K, N] that w stands for (what forward and
+    dense_ffn take for larger batches)."""
+    if not isinstance(w, W4Weights):
+        raise TypeError("w must be W4Weights (w4_pack, w4_quantize)")
+    dev = w.data.device
+    o = torch.empty(w.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+    po = _same(o, "out", torch.bfloat16, w.shape, dev)
+    _check(load().moe_w4_dequantize_weights(w.data.data_ptr(), w.E, w.K, w.N, w.group, w.flags, po,
+                                            _raw_stream(dev)), "moe_w4_dequantize_weights")
+    return o
+
+
+@_on_device
+def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None,
+              fp32: bool = False) -> torch.Tensor:
+    """moe_linear_w4: y = x W for x bf16 [T, K], T <= 16, and one 4-bit matrix -> y [T, N], bf16
+    (or fp32 with fp32=True).  stream=: run on that stream."""
+    if not isinstance(w, W4Weights):
+        raise TypeError("w must be W4Weights (w4_pack, w4_quantize)")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
+    T, K = x.shape
+    dev = x.device
+    px = _dev(x, "x", torch.bfloat16, (T, w.K))
+    pw = _w4(w, "w", 1, K, w.N, dev)
+    dt = torch.float32 if fp32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((T, w.N), dtype=dt, device=dev)
+        py = out.data_ptr()
+    else:
+        py = _same(out, "out", dt, (T, w.N), dev)
+    if T:
+        _check(load().moe_linear_w4(px, pw, T, K, w.N, w.group,
+                                    w.flags | (MOE_FLAG_F32_OUT if fp32 else 0), py,
+                                    _raw_stream(dev)), "moe_linear_w4")
+    return out
+
+
+def _w4_workspace(nbytes: int, given: torch.Tensor | None, what: str, dev) -> torch.Tensor:
+    """The call's own scratch (torch's allocator ties it to the current stream, or to the graph
+    being captured, so calls on other streams and other graphs never share it), or the caller's."""
+    if nbytes == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, what)
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _same(given, "workspace_buf", torch.uint8, (given.numel(),), dev)
+    return given
+
+
+def _w4_same_form(*ws: W4Weights) -> None:
+    if any(w.group != ws[0].group or w.zeros != ws[0].zeros for w in ws):
+        raise ValueError("the matrices of one layer must share group and zeros")
+
+
+@_on_device
+def dense_ffn_w4(x: torch.Tensor, w_gate: W4Weights, w_up: W4Weights, w_down: W4Weights,
+                 out: torch.Tensor | None = None,
+                 workspace_buf: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_dense_ffn_w4: dense_ffn with 4-bit weights for T <= 16 tokens -> y bf16 [T, H]:
+    y = (gelu_tanh(x W_gate) * (x W_up)) W_down.  stream=: run on that stream."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
+    T, H = x.shape
+    dev = x.device
+    if not isinstance(w_gate, W4Weights):
+        raise TypeError("w_gate must be W4Weights (w4_pack, w4_quantize)")
+    I = w_gate.N
+    px = _dev(x, "x", torch.bfloat16, (T, H))
+    pg = _w4(w_gate, "w_gate", 1, H, I, dev)
+    pu = _w4(w_up, "w_up", 1, H, I, dev)
+    pd = _w4(w_down, "w_down", 1, I, H, dev)
+    _w4_same_form(w_gate, w_up, w_down)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
+    py = _same(y, "out", torch.bfloat16, (T, H), dev)
+    if T == 0:
+        return y
+    L = load()
+    ws = _w4_workspace(L.moe_dense_w4_workspace_size(T, H, I), workspace_buf,
+                       "moe_dense_w4_workspace_size", dev)
+    _check(L.moe_dense_ffn_w4(px, pg, pu, pd, T, H, I, w_gate.group, w_gate.flags, py,
+                              ws.data_ptr(), ws.numel(), _raw_stream(dev)), "moe_dense_ffn_w4")
+    return y
+
+
+@_on_device
+def forward_w4(x: torch.Tensor, w_router: torch.Tensor, w_gate: W4Weights, w_up: W4Weights,
+               w_down: W4Weights, k: int, bias: torch.Tensor | None = None, renorm: bool = True,
+               aux: bool = False, out: torch.Tensor | None = None,
+               workspace_buf: torch.Tensor | None = None):
+    """moe_forward_w4: the routed layer with 4-bit expert weights for T <= 16 tokens -> y bf16
+    [T, H] (and the routing dict of forward if aux).  stream=: run on that stream."""
+    if x.dim() != 2 or w_router.dim() != 2:
+        raise ValueError("x must be [T, H] and w_router [H, E]")
+    T, H = x.shape
+    E = w_router.shape[1]
+    dev = x.device
+    if not isinstance(w_gate, W4Weights):
+        raise TypeError("w_gate must be W4Weights (w4_pack, w4_quantize)")
+    I = w_gate.N
+    px = _dev(x, "x", torch.bfloat16, (T, H))
+    pr = _same(w_router, "w_router", torch.bfloat16, (H, E), dev)
+    pb = None if bias is None else _same(bias, "bias", torch.float32, (E,), dev)
+    pg = _w4(w_gate, "w_gate", E, H, I, dev)
+    pu = _w4(w_up, "w_up", E, H, I, dev)
+    pd = _w4(w_down, "w_down", E, I, H, dev)
+    _w4_same_form(w_gate, w_up, w_down)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
+    py = _same(y, "out", torch.bfloat16, (T, H), dev)
+    a, aux_d = _aux_out(T, E, k, dev) if aux else (None, None)
+    if T == 0:
+        return (y, aux_d) if aux else y
+    L = load()
+    flags = w_gate.flags | (0 if renorm else MOE_FLAG_NO_RENORM)
+    ws = _w4_workspace(L.moe_w4_workspace_size(T, H, E, I, k, flags), workspace_buf,
+                       "moe_w4_workspace_size", dev)
+    _check(L.moe_forward_w4(px, pr, pb, pg, pu, pd, T, H, E, I, k, w_gate.group, flags, py,
+                            None if a is None else ctypes.byref(a), ws.data_ptr(), ws.numel(),
+                            _raw_stream(dev)), "moe_forward_w4")
+    return (y, aux_d) if aux else y
+
+
+def _aux_out(T: int, E: int, k: int, dev) -> tuple[AuxOut, dict]:
+    aux_d = {
+        "expert_counts": torch.empty(E, dtype=torch.int32, device=dev),
+        "expert_offsets": torch.empty(E + 1, dtype=torch.int32, device=dev),
+        "perm": torch.empty(T * k, dtype=torch.int32, device=dev),
+        "topk_ids": torch.empty((T, k), dtype=torch.int32, device=dev),
+        "topk_weights": torch.empty((T, k), dtype=torch.float32, device=dev),
+        "router_stats": torch.zeros(5, dtype=torch.int32, device=dev),
+    }
+    return AuxOut(*(aux_d[n].data_ptr() for n, _ in AuxOut._fields_)), aux_d
 
 
 def router_stats(aux: dict) -> dict:

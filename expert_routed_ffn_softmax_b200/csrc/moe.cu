@@ -1534,3 +1534,5 @@ moe_status_t moe_debug_unsatisfied_wait(void* stream) {
 }
 
 }  // extern "C"
+
+#include "w4_abi.cuh"

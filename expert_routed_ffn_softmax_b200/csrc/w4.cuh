@@ -1,0 +1,282 @@
+// w4.cuh -- 4-bit weights with one bf16 scale (and optionally one zero point) per group of
+// 32, 64 or 128 consecutive elements along the reduction axis, activations left in bf16:
+//
+//     value(n, k) = (code(n, k) - zero(n, k / group)) * scale(n, k / group)
+//
+// with code and zero in 0..15 (zero = 8 everywhere in the symmetric form).
+//
+// This file holds the packed layout, the way into it (from bf16 weights or from a checkpoint's
+// codes and scales), the way back to bf16, and the 16-row x 64-deep product of one packed block
+// with up to 16 activation rows that the few-token kernels are built from.
+//
+// Packed layout.  A matrix of N outputs and reduction depth K is cut into strips of 16 rows
+// (outputs) and blocks of 64 elements along K; record (strip, block) holds everything the
+// block's product needs, so that a strip is one contiguous byte range and any run of its
+// blocks is one bulk copy:
+//   512 bytes of codes: 16 bytes per lane of the warp that multiplies the block.  Lane
+//       l = 4 g + t holds rows g and g + 8, elements 8 t .. 8 t + 7 of each 32-element half:
+//       words (row g, half 0), (row g + 8, half 0), (row g, half 1), (row g + 8, half 1).  In a
+//       word, nibble i < 4 is element 2 i and nibble 4 + i is element 2 i + 1, so that the mask
+//       0x000F000F of the word shifted by 4 i is a pair of neighbours in the halves of a
+//       register: an operand register of the matrix instruction after two operations.
+//   then 32 bytes per group of the block (two groups of 32, else one): bf16 scales, rows
+//       interleaved 0, 8, 1, 9, .. 7, 15 (one 4-byte read gives a lane both of its rows);
+//       a 128-element group repeats its scales in both of its blocks (3 % of the bytes, in
+//       return for blocks that stand alone);
+//   then, asymmetric form only, 16 bytes per group of the block: zero points, same row order.
+#pragma once
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int W4_ROWS = 16;      // rows of a strip
+constexpr int W4_KB = 64;        // elements of a block along K
+constexpr int W4_MAX_T = 16;     // activation rows of the few-token kernels
+
+// Groups of one block, and the bytes of one record.
+__host__ __device__ constexpr int w4_groups(int group) { return group == 32 ? 2 : 1; }
+__host__ __device__ constexpr int w4_record(int group, bool zeros) {
+  return 512 + w4_groups(group) * (zeros ? 48 : 32);
+}
+__host__ __device__ inline size_t w4_matrix_bytes(int K, int N, int group, bool zeros) {
+  return (size_t)(N / W4_ROWS) * (K / W4_KB) * w4_record(group, zeros);
+}
+
+// Eight codes in element order (element j in nibble j) -> the word order above.
+__device__ __forceinline__ uint32_t w4_interleave(uint32_t w) {
+  auto squeeze = [](uint32_t v) {   // nibbles 0, 2, 4, 6 of v -> nibbles 0..3
+    v &= 0x0F0F0F0Fu;
+    v = (v | (v >> 4)) & 0x00FF00FFu;
+    return (v | (v >> 8)) & 0xFFFFu;
+  };
+  return squeeze(w) | (squeeze(w >> 4) << 16);
+}
+// Nibble of element j (0..7) in a packed word.
+__device__ __forceinline__ uint32_t w4_nibble(uint32_t w, int j) {
+  return (w >> (4 * ((j >> 1) + 4 * (j & 1)))) & 15u;
+}
+// Position of row r (0..15) in a group's scales and zero points.
+__device__ __forceinline__ int w4_row_slot(int r) { return 2 * (r & 7) + (r >> 3); }
+
+// ----------------------------------------------------------------------------- into the layout
+// A tile of the packing kernels: 64 rows x 128 elements (4 strips x 2 blocks; ragged at the
+// matrix's ends), assembled in shared memory and written as runs of two records per strip.
+constexpr int W4_TILE_N = 64, W4_TILE_K = 128;
+constexpr int W4_TILE_BYTES = 4 * 2 * 608;
+
+// Write the assembled records [strip][block][R] of tile (n0, k0) of matrix `e`.
+__device__ __forceinline__ void w4_store_tile(const uint8_t* rec, uint8_t* packed, int e, int n0,
+                                              int k0, int K, int N, int R) {
+  const int strips = min(4, (N - n0) / W4_ROWS), blocks = min(2, (K - k0) / W4_KB);
+  const int vec = blocks * R / 16;   // 16-byte vectors per strip: contiguous in both places
+  const size_t kb = K / W4_KB;
+  for (int i = threadIdx.x; i < strips * vec; i += blockDim.x) {
+    const int s = i / vec, v = i - s * vec;
+    uint8_t* dst = packed + (((size_t)e * (N / W4_ROWS) + n0 / W4_ROWS + s) * kb + k0 / W4_KB) * R;
+    reinterpret_cast<uint4*>(dst)[v] = *reinterpret_cast<const uint4*>(rec + s * 2 * R + 16 * v);
+  }
+}
+
+// codes uint8 [E][N][K/2] (element 2b in the low nibble of byte b), scales bf16 [E][N][G],
+// zeros uint8 [E][N][G] or null (G = ceil(K / group)) -> packed.  Only the low nibble of a zero
+// point is kept.  Bound by its bytes: each thread moves 16 bytes (32 codes of one row).
+__global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict__ codes,
+                                                      const __nv_bfloat16* __restrict__ scales,
+                                                      const uint8_t* __restrict__ zeros, int K,
+                                                      int N, int group, uint8_t* __restrict__ packed) {
+  __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
+  const bool zp = zeros != nullptr;
+  const int R = w4_record(group, zp), gpb = w4_groups(group), G = (K + group - 1) / group;
+  const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
+  const int row = threadIdx.x >> 2, part = threadIdx.x & 3;   // 32 elements of one row
+  const int n = n0 + row, k = k0 + 32 * part;
+  if (n < N && k < K) {
+    const size_t at = (size_t)e * N + n;
+    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(codes + at * (K / 2) + k / 2));
+    const int strip = row >> 4, r = row & 15, block = part >> 1, half = part & 1;
+    uint8_t* b = rec + (strip * 2 + block) * R;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      *reinterpret_cast<uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half + 4 * (r >> 3)) =
+          w4_interleave(w[t]);
+    if (half == 0 || gpb == 2) {
+      const int gi = half * (gpb - 1);
+      const size_t ga = at * G + k / group;
+      reinterpret_cast<__nv_bfloat16*>(b + 512)[gi * 16 + w4_row_slot(r)] = scales[ga];
+      if (zp) b[512 + gpb * 32 + gi * 16 + w4_row_slot(r)] = zeros[ga] & 15;
+    }
+  }
+  __syncthreads();
+  w4_store_tile(rec, packed, e, n0, k0, K, N, R);
+}
+
+// bf16 weights w [E][K][N] (N contiguous) -> packed.  Per group, in fp32, every step one
+// rounding to nearest even: symmetric scale = bf16(max |w| / 7), code = clamp(rint(w / scale)
+// + 8, 0, 15); asymmetric lo = min(w, 0), hi = max(w, 0), scale = bf16((hi - lo) / 15), zero =
+// clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15).  A zero scale
+// gives codes and zero points of 8.  Bound by its bytes (2.5 to 2.6 per weight).
+template <bool ZP>
+__global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K,
+                                                          int N, int group,
+                                                          uint8_t* __restrict__ packed) {
+  __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
+  __shared__ float s_lo[4][W4_TILE_N], s_hi[4][W4_TILE_N];
+  const int R = w4_record(group, ZP), gpb = w4_groups(group);
+  const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
+  const int row = threadIdx.x & 63, part = threadIdx.x >> 6;   // 32 elements of one row
+  const int n = n0 + row, k = k0 + 32 * part;
+  const bool in = n < N && k < K;
+  float v[32];
+  float lo = 0.f, hi = 0.f;
+  if (in) {
+    const __nv_bfloat16* p = w + ((size_t)e * K + k) * N + n;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __bfloat162float(p[(size_t)i * N]);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      lo = fminf(lo, v[i]);
+      hi = fmaxf(hi, v[i]);
+    }
+  }
+  s_lo[part][row] = lo;
+  s_hi[part][row] = hi;
+  __syncthreads();
+  if (in) {
+    const int span = group / 32, p0 = part / span * span;   // the 32-element parts of the group
+    for (int i = p0; i < p0 + span; ++i) {
+      lo = fminf(lo, s_lo[i][row]);
+      hi = fmaxf(hi, s_hi[i][row]);
+    }
+    const __nv_bfloat16 sb = __float2bfloat16_rn(ZP ? __fdiv_rn(__fsub_rn(hi, lo), 15.f)
+                                                    : __fdiv_rn(fmaxf(-lo, hi), 7.f));
+    const float s = __bfloat162float(sb);
+    const float z = ZP && s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 8.f;
+    const int strip = row >> 4, r = row & 15, block = part >> 1, half = part & 1;
+    uint8_t* b = rec + (strip * 2 + block) * R;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = s > 0.f ? rintf(__fdiv_rn(v[8 * t + j], s)) + z : z;
+        word |= (uint32_t)(int)fminf(fmaxf(q, 0.f), 15.f) << (4 * ((j >> 1) + 4 * (j & 1)));
+      }
+      *reinterpret_cast<uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half + 4 * (r >> 3)) = word;
+    }
+    if (half == 0 || gpb == 2) {
+      const int gi = half * (gpb - 1);
+      reinterpret_cast<__nv_bfloat16*>(b + 512)[gi * 16 + w4_row_slot(r)] = sb;
+      if (ZP) b[512 + gpb * 32 + gi * 16 + w4_row_slot(r)] = (uint8_t)z;
+    }
+  }
+  __syncthreads();
+  w4_store_tile(rec, packed, e, n0, k0, K, N, R);
+}
+
+// packed -> bf16 w [E][K][N]: each value rounded once (the difference of the codes is exact, its
+// product with the scale has at most 12 significant bits).
+__global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __restrict__ packed, int K,
+                                                            int N, int group, int zeros,
+                                                            __nv_bfloat16* __restrict__ w) {
+  const int R = w4_record(group, zeros), gpb = w4_groups(group);
+  const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
+  const int row = threadIdx.x & 63, part = threadIdx.x >> 6;
+  const int n = n0 + row, k = k0 + 32 * part;
+  if (n >= N || k >= K) return;
+  const int r = row & 15, half = part & 1;
+  const uint8_t* b = packed + (((size_t)e * (N / W4_ROWS) + n / W4_ROWS) * (K / W4_KB) + k / W4_KB) * R;
+  const int gi = half * (gpb - 1);
+  const float s = __bfloat162float(
+      reinterpret_cast<const __nv_bfloat16*>(b + 512)[gi * 16 + w4_row_slot(r)]);
+  const float z = zeros ? (float)b[512 + gpb * 32 + gi * 16 + w4_row_slot(r)] : 8.f;
+  __nv_bfloat16* p = w + ((size_t)e * K + k) * N + n;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t word = *reinterpret_cast<const uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half +
+                                                             4 * (r >> 3));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      p[(size_t)(8 * t + j) * N] =
+          __float2bfloat16_rn(__fmul_rn((float)w4_nibble(word, j) - z, s));
+  }
+}
+
+// ----------------------------------------------------------------------------- the block product
+// D += A B for 16 x 16 A (row-major), 16 x 8 B, bf16 in, fp32 accumulation.  tcgen05.mma would
+// need the decoded weights in shared or tensor memory: a write and a read of four times the
+// bytes that arrive.  Here a lane decodes its 16 bytes in registers, which are already the
+// instruction's operand, and at 16 activation rows the products are far from either rate.
+__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes of nibbles i and 4 + i as a pair of exact bf16 integers code - zero; z2 = 128 + zero in
+// both halves.  0x4300 is 128 in bf16, whose unit in the last place is 1: the code takes the
+// low bits, and the subtraction is exact.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i, uint32_t z2) {
+  const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&z2));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// One group's zero points of a lane's two rows, as the subtrahends of w4_pair.
+__device__ __forceinline__ void w4_zero_pair(uint32_t two, uint32_t& z_lo, uint32_t& z_hi) {
+  z_lo = (two & 0xffu) * 0x00010001u + 0x43004300u;
+  z_hi = ((two >> 8) & 0xffu) * 0x00010001u + 0x43004300u;
+}
+
+// acc[j] += block (record at `rec`, this warp's lane) * activation fragments.  xf[h][j]: the
+// lane's 8 activations (elements 32 h + 8 t .. + 7 of row g + 8 j, for lane 4 g + t).  acc[j]:
+// (row g, activation rows 8 j + 2 t and + 1), (row g + 8, the same).  The products of a group are
+// exact integers times bf16, summed in fp32 by the matrix instruction; the scale is applied once
+// per group, in fp32, so nothing is rounded to bf16 on the way.
+template <int NB, bool G32, bool ZP>
+__device__ __forceinline__ void w4_block(float (&acc)[NB][4], const uint8_t* rec, int lane,
+                                         const uint4 (&xf)[2][NB]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(rec + 16 * lane);
+  const int g = lane >> 2;
+  constexpr int GPB = G32 ? 2 : 1;
+  float p[NB][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = h ? q.z : q.x, hi = h ? q.w : q.y;
+    uint32_t z_lo = 0x43084308u, z_hi = 0x43084308u;
+    if (ZP)
+      w4_zero_pair(*reinterpret_cast<const uint16_t*>(rec + 512 + GPB * 32 + (G32 ? 16 * h : 0) + 2 * g),
+                   z_lo, z_hi);
+    if (G32 || h == 0) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[j][i] = 0.f;
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t a0 = w4_pair(lo, 2 * s, z_lo), a1 = w4_pair(hi, 2 * s, z_hi);
+      const uint32_t a2 = w4_pair(lo, 2 * s + 1, z_lo), a3 = w4_pair(hi, 2 * s + 1, z_hi);
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        w4_mma(p[j], a0, a1, a2, a3, s ? xf[h][j].z : xf[h][j].x, s ? xf[h][j].w : xf[h][j].y);
+    }
+    if (G32 || h == 1) {
+      const uint32_t s2 = *reinterpret_cast<const uint32_t*>(rec + 512 + (G32 ? 32 * h : 0) + 4 * g);
+      const float s_lo = __uint_as_float(s2 << 16), s_hi = __uint_as_float(s2 & 0xffff0000u);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        acc[j][0] = fmaf(s_lo, p[j][0], acc[j][0]);
+        acc[j][1] = fmaf(s_lo, p[j][1], acc[j][1]);
+        acc[j][2] = fmaf(s_hi, p[j][2], acc[j][2]);
+        acc[j][3] = fmaf(s_hi, p[j][3], acc[j][3]);
+      }
+    }
+  }
+}
+
+}  // namespace moe

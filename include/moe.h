@@ -99,7 +99,11 @@ enum {
    * is moe_ffn_kernel_name()'s choice; setting both, or either with a static or decode tile
    * family, is MOE_ERR_INVALID_ARG; at 64 tokens or fewer both are ignored. */
   MOE_FLAG_FFN_ROWS_COPY = 1u << 10,
-  MOE_FLAG_FFN_ROWS_GATHER = 1u << 11
+  MOE_FLAG_FFN_ROWS_GATHER = 1u << 11,
+  /* The 4-bit calls (moe_*w4*) only: the packed weights hold zero points (asymmetric form). */
+  MOE_FLAG_W4_ZEROS = 1u << 12,
+  /* moe_linear_w4 only: y in fp32 instead of bf16. */
+  MOE_FLAG_F32_OUT = 1u << 13
 };
 
 /* Optional caller-owned device outputs of moe_forward (any member may be NULL). */
@@ -321,6 +325,86 @@ moe_status_t moe_forward_nvfp4(const void *x, const void *w_router, const float 
                                unsigned flags, float act_scale_x, float act_scale_h, void *y,
                                const moe_aux_t *aux, void *workspace, size_t workspace_bytes,
                                void *stream);
+
+/*
+ * 4-bit weights, bf16 activations (few tokens).  A weight is a 4-bit code with one bf16 scale
+ * and, in the asymmetric form, one 4-bit zero point per group of `group` = 32, 64 or 128
+ * consecutive elements along the reduction axis K (the last group of a row may be shorter):
+ *     value(n, k) = (code(n, k) - zero(n, k / group)) * scale(n, k / group),   codes 0..15,
+ * with zero = 8 everywhere in the symmetric form.  The page's checkpoint of this size class is
+ * NVFP4 (above); this form keeps the activations in bf16, so the layer's only quantisation error
+ * is the weights'.  The pages name no such format: the layer's formulas are those of moe_forward
+ * and moe_dense_ffn with these weights.
+ *
+ * A matrix with reduction depth K and N outputs is kept packed: moe_w4_packed_bytes(E, K, N,
+ * group, flags) bytes for E matrices back to back, 16-byte aligned, each [N/16][K/64] records of
+ * R = 512 + g * (zeros ? 48 : 32) bytes, g = 2 for group 32 and 1 otherwise.  Record (strip s,
+ * block b) covers rows 16 s .. + 15 and elements 64 b .. + 63: bytes 0..511 hold the codes, 16
+ * bytes for each lane l = 4 i + t (0 <= i < 8, 0 <= t < 4) as four little-endian words (row i,
+ * elements 8 t .. + 7), (row i + 8, the same), (row i, elements 32 + 8 t .. + 7), (row i + 8, the
+ * same), where nibbles 0..3 of a word are its elements 0, 2, 4, 6 and nibbles 4..7 its elements
+ * 1, 3, 5, 7; then per group 16 bf16 scales, rows in the order 0, 8, 1, 9, .. 7, 15; then,
+ * with zero points, 16 bytes per group in the same order.  A 128-element group has its scales in
+ * both of its blocks.
+ *
+ * Limits of every call of this section: 64 <= K <= 16384, K % 64 == 0; 16 <= N <= 1048576,
+ * N % 16 == 0; E <= 4096; group 32, 64 or 128 (else MOE_ERR_INVALID_ARG).  `flags` must say
+ * MOE_FLAG_W4_ZEROS exactly when the packed weights hold zero points.  Scales must be finite.
+ * The products compute with exact integers code - zero, sums in fp32, the scale applied in fp32.
+ */
+
+/* Bytes of E packed matrices (0 = unsupported shape).  flags: MOE_FLAG_W4_ZEROS. */
+size_t moe_w4_packed_bytes(int E, int K, int N, int group, unsigned flags);
+
+/* A checkpoint's matrices -> packed.  codes uint8 [E][N][K/2] (byte b of a row holds element 2b
+ * in its low nibble, 2b+1 in its high nibble; 16-byte aligned), scales bf16 [E][N][G], zeros
+ * uint8 [E][N][G] (values 0..15; the high nibble is ignored) or NULL for the symmetric form,
+ * G = ceil(K / group). */
+moe_status_t moe_w4_pack(const uint8_t *codes, const void *scales, const uint8_t *zeros, int E,
+                         int K, int N, int group, void *packed, void *stream);
+
+/* bf16 weights w [E][K][N] (N contiguous, the layout moe_forward takes) -> packed.  Per group, in
+ * fp32, each step rounding to nearest even:
+ *   symmetric:  scale = bf16(max |w| / 7);  code = clamp(rint(w / scale) + 8, 0, 15)
+ *   MOE_FLAG_W4_ZEROS:  lo = min(w, 0), hi = max(w, 0);  scale = bf16((hi - lo) / 15);
+ *               zero = clamp(rint(-lo / scale), 0, 15);  code = clamp(rint(w / scale) + zero, 0, 15)
+ * and code = zero = 8 where scale == 0. */
+moe_status_t moe_w4_quantize_weights(const void *w, int E, int K, int N, int group, unsigned flags,
+                                     void *packed, void *stream);
+
+/* packed -> bf16 w [E][K][N]: each value rounded once to bf16.  The way to run larger batches
+ * through moe_forward / moe_dense_ffn with the same weights. */
+moe_status_t moe_w4_dequantize_weights(const void *packed, int E, int K, int N, int group,
+                                       unsigned flags, void *w, void *stream);
+
+/* y = x W for 0 <= T <= 16 rows: x bf16 [T, K], w packed (E = 1), y bf16 [T, N], or fp32 with
+ * MOE_FLAG_F32_OUT (logits).  x, w and y 16-byte aligned; y may not alias x.  No workspace. */
+moe_status_t moe_linear_w4(const void *x, const void *w, int T, int K, int N, int group,
+                           unsigned flags, void *y, void *stream);
+
+/* The dense GEGLU MLP of moe_dense_ffn with 4-bit weights, T <= 16: w_gate, w_up packed (K = H,
+ * N = I), w_down packed (K = I, N = H).  h is rounded to bf16 between the two products, as in
+ * moe_dense_ffn.  H, I multiples of 64, H <= 16384, I <= 8192.  Workspace:
+ * moe_dense_w4_workspace_size bytes (0 = unsupported shape). */
+size_t moe_dense_w4_workspace_size(int T, int H, int I);
+moe_status_t moe_dense_ffn_w4(const void *x, const void *w_gate, const void *w_up,
+                              const void *w_down, int T, int H, int I, int group, unsigned flags,
+                              void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * moe_forward_w4 -- the routed layer with 4-bit expert weights for batches of T <= 16 tokens.
+ * Router as moe_route (bf16 w_router; the same ids and weights), experts as moe_forward: w_gate,
+ * w_up E packed matrices (K = H, N = I), w_down E packed matrices (K = I, N = H).  h is rounded
+ * to bf16; the expert outputs and their weighted sum stay in fp32 until y.  flags:
+ * MOE_FLAG_NO_RENORM, MOE_FLAG_W4_ZEROS.  aux as moe_forward.  Shapes as moe_forward, T <= 16.
+ * Workspace: moe_w4_workspace_size bytes (0 = unsupported shape).
+ */
+size_t moe_w4_workspace_size(int T, int H, int E, int I, int k, unsigned flags);
+moe_status_t moe_forward_w4(const void *x, const void *w_router, const float *router_bias,
+                            const void *w_gate, const void *w_up, const void *w_down, int T, int H,
+                            int E, int I, int k, int group, unsigned flags, void *y,
+                            const moe_aux_t *aux, void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /*
  * moe_route_static -- moe_route for callers that cannot allocate device memory.
