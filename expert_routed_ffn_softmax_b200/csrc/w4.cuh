@@ -16,9 +16,9 @@
 //   512 bytes of codes: 16 bytes per lane of the warp that multiplies the block.  Lane
 //       l = 4 g + t holds rows g and g + 8, elements 8 t .. 8 t + 7 of each 32-element half:
 //       words (row g, half 0), (row g + 8, half 0), (row g, half 1), (row g + 8, half 1).  In a
-//       word, nibble i < 4 is element 2 i and nibble 4 + i is element 2 i + 1, so that the mask
-//       0x000F000F of the word shifted by 4 i is a pair of neighbours in the halves of a
-//       register: an operand register of the matrix instruction after two operations.
+//       word, nibble i < 4 is element 2 i and nibble 4 + i is element 2 i + 1, so that one mask
+//       leaves a pair of neighbours in the halves of a register, as the operands of the matrix
+//       instruction want them.
 //   then 32 bytes per group of the block (two groups of 32, else one): bf16 scales, rows
 //       interleaved 0, 8, 1, 9, .. 7, 15 (one 4-byte read gives a lane both of its rows);
 //       a 128-element group repeats its scales in both of its blocks (3 % of the bytes, in
@@ -203,77 +203,130 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __res
 }
 
 // ----------------------------------------------------------------------------- the block product
-// D += A B for 16 x 16 A (row-major), 16 x 8 B, bf16 in, fp32 accumulation.  tcgen05.mma would
+// D = A B (+ D unless `clear`, a constant) for 16 x 16 A (row-major), 16 x 8 B, bf16 in, fp32 accumulation.  tcgen05.mma would
 // need the decoded weights in shared or tensor memory: a write and a read of four times the
 // bytes that arrive.  Here a lane decodes its 16 bytes in registers, which are already the
 // instruction's operand, and at 16 activation rows the products are far from either rate.
+// (Not volatile: the compiler may interleave independent chains.)
 __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                       uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                       uint32_t a3, uint32_t b0, uint32_t b1, bool clear) {
+  const float c0 = clear ? 0.f : d[0], c1 = clear ? 0.f : d[1];
+  const float c2 = clear ? 0.f : d[2], c3 = clear ? 0.f : d[3];
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Codes of nibbles i and 4 + i as a pair of exact bf16 integers code - zero; z2 = 128 + zero in
-// both halves.  0x4300 is 128 in bf16, whose unit in the last place is 1: the code takes the
-// low bits, and the subtraction is exact.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i, uint32_t z2) {
-  const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&z2));
-  return *reinterpret_cast<const uint32_t*>(&d);
+// Decoding.  A pair of codes becomes a pair of exact bf16 values (code - zero) / 4 in one logical
+// operation and one fused multiply-add; the 4 goes into the group's scale.  The logical pipe is
+// the scarce one (half the issue rate), so the shifts are kept to one per eight codes:
+//   nibbles 0 and 4 of a word: OR with 0x4300 makes 128 + code (whose unit in the last place is
+//       1), times 1/4, minus (128 + zero) / 4;
+//   nibbles 1 and 5 stay where they are: a bf16 with nothing above bit 7 is its low byte times
+//       2^-133, also when that is subnormal, so the masked pair is code * 2^-129; times 2^127,
+//       minus zero / 4;
+//   nibbles 2, 6 and 3, 7: the same after a shift by 8.
+struct W4Zero {
+  uint32_t a, b;   // -(128 + zero) / 4 and -zero / 4, in both halves
+};
+constexpr uint32_t W4_QUARTER = 0x3E803E80u, W4_2P127 = 0x7F007F00u;
+__device__ __forceinline__ uint32_t w4_fma(uint32_t v, uint32_t m, uint32_t a) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(m), "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t w4_low(uint32_t word, const W4Zero& z) {
+  return w4_fma((word & 0x000F000Fu) | 0x43004300u, W4_QUARTER, z.a);
+}
+__device__ __forceinline__ uint32_t w4_high(uint32_t word, const W4Zero& z) {
+  return w4_fma(word & 0x00F000F0u, W4_2P127, z.b);
+}
+// The subtrahends for a zero point in the low byte of `zero` (8 when symmetric).
+__device__ __forceinline__ W4Zero w4_zero(uint32_t zero) {
+  W4Zero z;
+  z.a = zero * 0x00010001u + 0xC200C200u;                     // -(32 + zero / 4)
+  z.b = w4_fma(z.a, 0x3F803F80u /* 1 */, 0x42004200u /* 32 */);
+  return z;
 }
 
-// One group's zero points of a lane's two rows, as the subtrahends of w4_pair.
-__device__ __forceinline__ void w4_zero_pair(uint32_t two, uint32_t& z_lo, uint32_t& z_hi) {
-  z_lo = (two & 0xffu) * 0x00010001u + 0x43004300u;
-  z_hi = ((two >> 8) & 0xffu) * 0x00010001u + 0x43004300u;
+// Reads at a 32-bit shared-memory address plus a constant (a generic pointer would cost a generic
+// load's address check, an added register an addition).
+template <int OFF>
+__device__ __forceinline__ uint4 lds_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(v) : "r"(at), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v) : "r"(at), "n"(OFF));
+  return v;
 }
 
-// acc[j] += block (record at `rec`, this warp's lane) * activation fragments.  xf[h][j]: the
-// lane's 8 activations (elements 32 h + 8 t .. + 7 of row g + 8 j, for lane 4 g + t).  acc[j]:
-// (row g, activation rows 8 j + 2 t and + 1), (row g + 8, the same).  The products of a group are
-// exact integers times bf16, summed in fp32 by the matrix instruction; the scale is applied once
-// per group, in fp32, so nothing is rounded to bf16 on the way.
-template <int NB, bool G32, bool ZP>
-__device__ __forceinline__ void w4_block(float (&acc)[NB][4], const uint8_t* rec, int lane,
-                                         const uint4 (&xf)[2][NB]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(rec + 16 * lane);
-  const int g = lane >> 2;
+// acc[i][j] += block i * activation fragments, for the records of NS strips at the same place
+// along K, in shared memory: rec[i] = the record's address + 16 lane.  x[j]: the address of the
+// lane's 8 activations of the first half (elements 8 t .. + 7 of row g + 8 j, for lane 4 g + t).
+// acc[i][j]: (row g, activation rows 8 j + 2 t and + 1), (row g + 8, the same).  The products of
+// a group are exact integers (over 4) times bf16, summed in fp32 by the matrix instruction; the
+// scale is applied once per group, in fp32, so nothing is rounded to bf16 on the way.
+template <int NS, int NB, bool G32, bool ZP>
+__device__ __forceinline__ void w4_block(float (&acc)[NS][NB][4], const uint32_t (&rec)[NS], int lane,
+                                         const uint32_t (&x)[NB]) {
   constexpr int GPB = G32 ? 2 : 1;
-  float p[NB][4];
+  uint4 q[NS];
+  uint32_t sc[NS], zp[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    q[i] = lds_v4<0>(rec[i]);
+    sc[i] = rec[i] - 16 * lane + 4 * (lane >> 2);         // this lane's two rows' scales,
+    if (ZP) zp[i] = rec[i] - 16 * lane + 2 * (lane >> 2);   // and zero points
+  }
+  float p[NS][NB][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = h ? q.z : q.x, hi = h ? q.w : q.y;
-    uint32_t z_lo = 0x43084308u, z_hi = 0x43084308u;
-    if (ZP)
-      w4_zero_pair(*reinterpret_cast<const uint16_t*>(rec + 512 + GPB * 32 + (G32 ? 16 * h : 0) + 2 * g),
-                   z_lo, z_hi);
-    if (G32 || h == 0) {
+    uint4 xf[NB];
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+    for (int j = 0; j < NB; ++j) xf[j] = h ? lds_v4<64>(x[j]) : lds_v4<0>(x[j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[j][i] = 0.f;
-    }
+    for (int i = 0; i < NS; ++i) {
+      const uint32_t lo = h ? q[i].z : q[i].x, hi = h ? q[i].w : q[i].y;
+      W4Zero z_lo = {0xC208C208u, 0xC000C000u}, z_hi = z_lo;   // zero points of 8
+      if (ZP) {
+        const uint32_t two = G32 && h ? lds_u16<512 + GPB * 32 + 16>(zp[i]) : lds_u16<512 + GPB * 32>(zp[i]);
+        z_lo = w4_zero(two & 0xffu);
+        z_hi = w4_zero(two >> 8);
+      }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const uint32_t a0 = w4_pair(lo, 2 * s, z_lo), a1 = w4_pair(hi, 2 * s, z_hi);
-      const uint32_t a2 = w4_pair(lo, 2 * s + 1, z_lo), a3 = w4_pair(hi, 2 * s + 1, z_hi);
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t wl = s ? lo >> 8 : lo, wh = s ? hi >> 8 : hi;
+        const uint32_t a0 = w4_low(wl, z_lo), a1 = w4_low(wh, z_hi);
+        const uint32_t a2 = w4_high(wl, z_lo), a3 = w4_high(wh, z_hi);
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        w4_mma(p[j], a0, a1, a2, a3, s ? xf[h][j].z : xf[h][j].x, s ? xf[h][j].w : xf[h][j].y);
-    }
-    if (G32 || h == 1) {
-      const uint32_t s2 = *reinterpret_cast<const uint32_t*>(rec + 512 + (G32 ? 32 * h : 0) + 4 * g);
-      const float s_lo = __uint_as_float(s2 << 16), s_hi = __uint_as_float(s2 & 0xffff0000u);
+        for (int j = 0; j < NB; ++j)
+          w4_mma(p[i][j], a0, a1, a2, a3, s ? xf[j].z : xf[j].x, s ? xf[j].w : xf[j].y,
+                 s == 0 && (G32 || h == 0));
+      }
+      if (G32 || h == 1) {
+        const uint32_t s2 = G32 && h ? lds_u32<512 + 32>(sc[i]) : lds_u32<512>(sc[i]);
+        const float s_lo = 4.f * __uint_as_float(s2 << 16);
+        const float s_hi = 4.f * __uint_as_float(s2 & 0xffff0000u);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        acc[j][0] = fmaf(s_lo, p[j][0], acc[j][0]);
-        acc[j][1] = fmaf(s_lo, p[j][1], acc[j][1]);
-        acc[j][2] = fmaf(s_hi, p[j][2], acc[j][2]);
-        acc[j][3] = fmaf(s_hi, p[j][3], acc[j][3]);
+        for (int j = 0; j < NB; ++j) {
+          acc[i][j][0] = fmaf(s_lo, p[i][j][0], acc[i][j][0]);
+          acc[i][j][1] = fmaf(s_lo, p[i][j][1], acc[i][j][1]);
+          acc[i][j][2] = fmaf(s_hi, p[i][j][2], acc[i][j][2]);
+          acc[i][j][3] = fmaf(s_hi, p[i][j][3], acc[i][j][3]);
+        }
       }
     }
   }

@@ -2,7 +2,8 @@
 // that these kernels share the device error word with the others).
 #pragma once
 #include "w4.cuh"
-#include "w4_gemv.cuh"
+#include "w4_stream.cuh"
+#include "w4_moe.cuh"
 
 namespace moe {
 namespace {
@@ -12,36 +13,129 @@ bool w4_matrix_ok(int K, int N) {
   return K >= 64 && K <= 16384 && K % 64 == 0 && N >= 16 && N <= 1048576 && N % 16 == 0;
 }
 
-// Launch a kernel of the (activation tiles, group, zero point) family.
-template <int MODE>
-void w4_gemv(const Launch& launch, dim3 grid, const W4Gemv& a) {
-  auto go = [&](auto kernel) { launch(true, kernel, grid, dim3(256), 0, a); };
+// Call fn(activation tiles, 32-element groups, zero points) with the three as types.
+template <typename F>
+auto w4_by_form(int T, int group, bool zeros, F&& fn) {
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
   auto by_zero = [&](auto nb, auto g32) {
-    if (a.zeros) go(w4_gemv_kernel<decltype(nb)::value, decltype(g32)::value, true, MODE>);
-    else go(w4_gemv_kernel<decltype(nb)::value, decltype(g32)::value, false, MODE>);
+    return zeros ? fn(nb, g32, std::true_type{}) : fn(nb, g32, std::false_type{});
   };
   auto by_group = [&](auto nb) {
-    if (a.group == 32) by_zero(nb, std::true_type{});
-    else by_zero(nb, std::false_type{});
+    return group == 32 ? by_zero(nb, std::true_type{}) : by_zero(nb, std::false_type{});
   };
-  if (a.T <= 8) by_group(std::integral_constant<int, 1>{});
-  else by_group(std::integral_constant<int, 2>{});
+  return T <= 8 ? by_group(One{}) : by_group(Two{});
 }
 
+// CTAs of the streaming kernels that run at once.
+int w4_slots(const DeviceState& d) { return 2 * std::max(1, d.num_sms); }
+
+// log2 of the row groups (of two strips) per unit of a linear layer.  A taller unit reads the
+// activations less often and joins fewer partial sums; a lower one deals out more evenly.  The
+// cost of a choice is its rounds of units over the CTAs, each the unit's weight and activation
+// bytes plus what a unit costs apart from them, in bytes.
+int w4_row_groups(int T, int K, int N, int record, int slots) {
+  int best = 0;
+  double least = 0;
+  for (int lg = 0; lg < 4; ++lg) {
+    const int tall = 2 << lg, units = (N / W4_ROWS + tall - 1) / tall;
+    const double cost =
+        (units + slots - 1) / slots * ((double)tall * (K / W4_KB) * record + 2.0 * T * K + 6144.0);
+    if (lg == 0 || cost < least) {
+      least = cost;
+      best = lg;
+    }
+  }
+  return best;
+}
+
+// One linear layer (or the gate | up half of a GEGLU MLP) on the streaming kernel.
+template <int MODE>
+moe_status_t w4_stream(const Launch& launch, const DeviceState& d, W4Linear a, int group, bool zeros) {
+  const int slots = w4_slots(d);
+  a.lg = MODE == W4_GEGLU ? 0 : w4_row_groups(a.T, a.K, a.N, w4_record(group, zeros), slots);
+  a.units = MODE == W4_GEGLU ? a.N / W4_ROWS : (a.N / W4_ROWS + (2 << a.lg) - 1) >> (a.lg + 1);
+  w4_by_form(a.T, group, zeros, [&](auto nb, auto g32, auto zp) {
+    constexpr int NB = decltype(nb)::value;
+    launch(true, w4_linear_kernel<NB, decltype(g32)::value, decltype(zp)::value, MODE>,
+           dim3(std::min(a.units, slots)), dim3(W4S_THREADS), w4s_smem<NB>(), a);
+  });
+  return launched();
+}
+
+// Shared memory limits of the streaming kernels, once per device.
+template <int MODE>
+bool w4_linear_attrs() {
+  bool ok = true;
+  for (int f = 0; f < 8; ++f)
+    w4_by_form(f & 1 ? 16 : 8, f & 2 ? 32 : 64, f & 4, [&](auto nb, auto g32, auto zp) {
+      constexpr int NB = decltype(nb)::value;
+      ok = ok && cudaFuncSetAttribute(w4_linear_kernel<NB, decltype(g32)::value, decltype(zp)::value, MODE>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      w4s_smem<NB>()) == cudaSuccess;
+    });
+  return ok;
+}
+bool w4_moe_attrs() {
+  bool ok = true;
+  for (int f = 0; f < 8; ++f)
+    w4_by_form(f & 1 ? 16 : 8, f & 2 ? 32 : 64, f & 4, [&](auto nb, auto g32, auto zp) {
+      constexpr int NB = decltype(nb)::value;
+      ok = ok && cudaFuncSetAttribute(w4_moe_kernel<NB, decltype(g32)::value, decltype(zp)::value>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      w4s_smem<NB>()) == cudaSuccess;
+    });
+  return ok;
+}
+DeviceState* w4_device_state(int* dev) {
+  static bool done[kMaxDevices] = {};
+  static std::mutex mu;
+  DeviceState* d = device_state(dev);
+  if (!d) return nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!done[*dev]) {
+    if (!w4_linear_attrs<W4_LINEAR>() || !w4_linear_attrs<W4_LINEAR_F32>() ||
+        !w4_linear_attrs<W4_GEGLU>() || !w4_moe_attrs()) {
+      cuda_failed(cudaGetLastError());
+      return nullptr;
+    }
+    done[*dev] = true;
+  }
+  return d;
+}
+
+// Workspace of the routed layer: the front kernel's partial sums, ids and weights, counters, h and
+// the weighted expert outputs.
 struct W4Layout {
-  size_t h = 0, o = 0, total = 0;
+  size_t logit = 0, xn2 = 0, wn2 = 0, stats = 0, ids = 0, wts = 0, ctr = 0, h = 0, o = 0, total = 0;
+  int slices = 0, lg2 = 0, n_ctr = 0;
 };
-W4Layout w4_layout(size_t at, size_t pairs, int H, int I, bool routed) {
+W4Layout w4_layout(int T, int H, int E, int I, int k) {
   W4Layout L;
-  L.h = at;
-  at = align256(at + 2 * pairs * I);
-  L.o = at;
-  if (routed) at = align256(at + sizeof(float) * pairs * H);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = align256(at + bytes);
+    return o;
+  };
+  const size_t P = (size_t)T * k;
+  L.slices = H / W4M_SLICE;
+  // W_down units of 128 rows
+  L.lg2 = 2;
+  L.n_ctr = W4M_CTR_O + H / W4_ROWS;
+  L.logit = take(sizeof(double) * L.slices * T * E);
+  L.xn2 = take(sizeof(double) * L.slices * T);
+  L.wn2 = take(sizeof(double) * L.slices * E);
+  L.stats = take(5 * sizeof(unsigned));
+  L.ids = take(sizeof(int32_t) * P);
+  L.wts = take(sizeof(float) * P);
+  L.ctr = take(sizeof(int) * L.n_ctr);
+  L.h = take(2 * P * I);
+  L.o = take(sizeof(float) * P * H);
   L.total = at;
   return L;
 }
 constexpr unsigned kW4LayerFlags = MOE_FLAG_NO_RENORM | MOE_FLAG_W4_ZEROS;
-unsigned w4_router_flags(unsigned flags) { return (flags & MOE_FLAG_NO_RENORM) | MOE_FLAG_ROUTER_FP64; }
 
 }  // namespace
 }  // namespace moe
@@ -117,28 +211,25 @@ moe_status_t moe_linear_w4(const void* x, const void* w, int T, int K, int N, in
     return MOE_ERR_INVALID_ARG;
   if (T > W4_MAX_T || !w4_matrix_ok(K, N)) return MOE_ERR_UNSUPPORTED;
   int dev = 0;
-  if (!device_state(&dev)) return MOE_ERR_CUDA;
+  DeviceState* d = w4_device_state(&dev);
+  if (!d) return MOE_ERR_CUDA;
   t_kernels = 0;
-  W4Gemv a = {};
+  W4Linear a = {};
   a.w0 = static_cast<const uint8_t*>(w);
   a.act = static_cast<const __nv_bfloat16*>(x);
   a.out = y;
   a.T = T;
   a.K = K;
   a.N = N;
-  a.group = group;
-  a.zeros = (flags & MOE_FLAG_W4_ZEROS) ? 1 : 0;
-  a.act_div = 1;
+  const bool zeros = flags & MOE_FLAG_W4_ZEROS;
   const Launch launch{static_cast<cudaStream_t>(stream), true};
-  const dim3 grid((N + 31) / 32);
-  if (flags & MOE_FLAG_F32_OUT) w4_gemv<W4_F32>(launch, grid, a);
-  else w4_gemv<W4_BF16>(launch, grid, a);
-  return launched();
+  return (flags & MOE_FLAG_F32_OUT) ? w4_stream<W4_LINEAR_F32>(launch, *d, a, group, zeros)
+                                    : w4_stream<W4_LINEAR>(launch, *d, a, group, zeros);
 }
 
 size_t moe_dense_w4_workspace_size(int T, int H, int I) {
   if (T < 1 || T > W4_MAX_T || H < 64 || H > 16384 || H % 64 || I < 64 || I > 8192 || I % 64) return 0;
-  return w4_layout(0, T, H, I, false).total;
+  return align256(2 * (size_t)T * I);   // h
 }
 
 moe_status_t moe_dense_ffn_w4(const void* x, const void* w_gate, const void* w_up, const void* w_down,
@@ -152,14 +243,15 @@ moe_status_t moe_dense_ffn_w4(const void* x, const void* w_gate, const void* w_u
       !aligned16(y) || !aligned16(workspace) || x == y)
     return MOE_ERR_INVALID_ARG;
   if (moe_dense_w4_workspace_size(T, H, I) == 0) return MOE_ERR_UNSUPPORTED;
-  const W4Layout L = w4_layout(0, T, H, I, false);
-  if (workspace_bytes < L.total) return MOE_ERR_NO_WORKSPACE;
+  if (workspace_bytes < moe_dense_w4_workspace_size(T, H, I)) return MOE_ERR_NO_WORKSPACE;
   int dev = 0;
-  if (!device_state(&dev)) return MOE_ERR_CUDA;
+  DeviceState* d = w4_device_state(&dev);
+  if (!d) return MOE_ERR_CUDA;
   t_kernels = 0;
   const Launch launch{static_cast<cudaStream_t>(stream), true};
-  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + L.h);
-  W4Gemv a = {};
+  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(workspace);
+  const bool zeros = flags & MOE_FLAG_W4_ZEROS;
+  W4Linear a = {};
   a.w0 = static_cast<const uint8_t*>(w_gate);
   a.w1 = static_cast<const uint8_t*>(w_up);
   a.act = static_cast<const __nv_bfloat16*>(x);
@@ -167,26 +259,20 @@ moe_status_t moe_dense_ffn_w4(const void* x, const void* w_gate, const void* w_u
   a.T = T;
   a.K = H;
   a.N = I;
-  a.group = group;
-  a.zeros = (flags & MOE_FLAG_W4_ZEROS) ? 1 : 0;
-  a.act_div = 1;
-  w4_gemv<W4_GEGLU>(launch, dim3(I / 16), a);
-  if (const moe_status_t s = launched(); s != MOE_OK) return s;
+  if (const moe_status_t s = w4_stream<W4_GEGLU>(launch, *d, a, group, zeros); s != MOE_OK) return s;
   a.w0 = static_cast<const uint8_t*>(w_down);
   a.w1 = nullptr;
   a.act = h;
   a.out = y;
   a.K = I;
   a.N = H;
-  w4_gemv<W4_BF16>(launch, dim3((H + 31) / 32), a);
-  return launched();
+  a.early = 1;
+  return w4_stream<W4_LINEAR>(launch, *d, a, group, zeros);
 }
 
 size_t moe_w4_workspace_size(int T, int H, int E, int I, int k, unsigned flags) {
   if ((flags & ~kW4LayerFlags) || T > W4_MAX_T || !shape_supported(T, H, E, I, k, true)) return 0;
-  return w4_layout(make_layout(T, H, E, I, k, w4_router_flags(flags), true).total, (size_t)T * k, H, I,
-                   true)
-      .total;
+  return w4_layout(T, H, E, I, k).total;
 }
 
 moe_status_t moe_forward_w4(const void* x, const void* w_router, const float* router_bias,
@@ -203,64 +289,60 @@ moe_status_t moe_forward_w4(const void* x, const void* w_router, const float* ro
       !aligned16(w_down) || !aligned16(y) || !aligned16(workspace) || x == y)
     return MOE_ERR_INVALID_ARG;
   if (moe_w4_workspace_size(T, H, E, I, k, flags) == 0) return MOE_ERR_UNSUPPORTED;
-  const unsigned rflags = w4_router_flags(flags);
-  const Layout L = make_layout(T, H, E, I, k, rflags, true);
-  const W4Layout W = w4_layout(L.total, (size_t)T * k, H, I, true);
+  const W4Layout W = w4_layout(T, H, E, I, k);
   if (workspace_bytes < W.total) return MOE_ERR_NO_WORKSPACE;
   int dev = 0;
-  DeviceState* d = device_state(&dev);
+  DeviceState* d = w4_device_state(&dev);
   if (!d) return MOE_ERR_CUDA;
   t_kernels = 0;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int32_t* ids = (aux && aux->topk_ids) ? aux->topk_ids : reinterpret_cast<int32_t*>(ws + L.ids);
-  float* wts = (aux && aux->topk_weights) ? aux->topk_weights : reinterpret_cast<float*>(ws + L.wts);
-  int32_t* counts =
-      (aux && aux->expert_counts) ? aux->expert_counts : reinterpret_cast<int32_t*>(ws + L.counts);
-  int32_t* offsets = (aux && aux->expert_offsets) ? aux->expert_offsets
-                                                  : reinterpret_cast<int32_t*>(ws + L.offsets);
-  int32_t* perm = (aux && aux->perm) ? aux->perm : reinterpret_cast<int32_t*>(ws + L.perm);
-  unsigned* stats = (aux && aux->router_stats) ? aux->router_stats
-                                               : reinterpret_cast<unsigned*>(ws + L.stats);
-  int32_t* inv = reinterpret_cast<int32_t*>(ws + L.inv);
-  Profiler prof{d, st, false};
-  const RouteBufs rb{ids, wts, stats, counts, offsets, perm, inv};
-  if (const moe_status_t rs = route_and_dispatch(x, w_router, router_bias, T, H, E, k, rflags, rb, ws,
-                                                 L, *d, st, prof, false);
-      rs != MOE_OK)
-    return rs;
-  const Launch launch{st, true};
-  W4Gemv a = {};
-  a.w0 = static_cast<const uint8_t*>(w_gate);
-  a.w1 = static_cast<const uint8_t*>(w_up);
-  a.act = static_cast<const __nv_bfloat16*>(x);
-  a.out = ws + W.h;
-  a.tile_num = reinterpret_cast<int32_t*>(ws + L.tile_num);
-  a.tile_expert = reinterpret_cast<int32_t*>(ws + L.tile_expert);
-  a.tile_row0 = reinterpret_cast<int32_t*>(ws + L.tile_row0);
-  a.tile_rows = reinterpret_cast<int32_t*>(ws + L.tile_rows);
-  a.perm = perm;
+  W4Moe a = {};
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.wr = static_cast<const __nv_bfloat16*>(w_router);
+  a.bias = router_bias;
+  a.wg = static_cast<const uint8_t*>(w_gate);
+  a.wu = static_cast<const uint8_t*>(w_up);
+  a.wd = static_cast<const uint8_t*>(w_down);
+  double* logit = reinterpret_cast<double*>(ws + W.logit);
+  double* xn2 = reinterpret_cast<double*>(ws + W.xn2);
+  double* wn2 = reinterpret_cast<double*>(ws + W.wn2);
+  a.part_logit = logit;
+  a.part_xn2 = xn2;
+  a.part_wn2 = wn2;
+  a.slices = W.slices;
   a.T = T;
-  a.K = H;
-  a.N = I;
-  a.group = group;
-  a.zeros = (flags & MOE_FLAG_W4_ZEROS) ? 1 : 0;
-  a.act_div = k;
-  const int tiles = std::min(E, T * k);
-  w4_gemv<W4_GEGLU>(launch, dim3(I / 16, tiles), a);
+  a.H = H;
+  a.E = E;
+  a.I = I;
+  a.k = k;
+  a.renorm = (flags & MOE_FLAG_NO_RENORM) ? 0 : 1;
+  a.lg2 = W.lg2;
+  const double u = std::ldexp(1.0, -53), n = (double)H + 8.0;
+  a.beta_scale = 2.0 * (n * u / (1.0 - n * u)) * 1.01;
+  a.ids = (aux && aux->topk_ids) ? aux->topk_ids : reinterpret_cast<int32_t*>(ws + W.ids);
+  a.wts = (aux && aux->topk_weights) ? aux->topk_weights : reinterpret_cast<float*>(ws + W.wts);
+  a.stats = (aux && aux->router_stats) ? aux->router_stats : reinterpret_cast<unsigned*>(ws + W.stats);
+  a.counts = aux ? aux->expert_counts : nullptr;
+  a.offsets = aux ? aux->expert_offsets : nullptr;
+  a.perm = aux ? aux->perm : nullptr;
+  a.ctr = reinterpret_cast<int*>(ws + W.ctr);
+  a.h = reinterpret_cast<__nv_bfloat16*>(ws + W.h);
+  a.o = reinterpret_cast<float*>(ws + W.o);
+  a.y = static_cast<__nv_bfloat16*>(y);
+  const Launch launch{static_cast<cudaStream_t>(stream), true};
+  auto front = [&](auto kernel) {
+    launch(true, kernel, dim3(W.slices), dim3(W4M_FRONT_THREADS), 0, a.x, a.wr, T, H, E, logit, xn2, wn2,
+           a.ctr, W.n_ctr, a.stats);
+  };
+  if (T <= 2) front(w4_front_kernel<2>);
+  else if (T <= 8) front(w4_front_kernel<8>);
+  else front(w4_front_kernel<16>);
   if (const moe_status_t s = launched(); s != MOE_OK) return s;
-  a.w0 = static_cast<const uint8_t*>(w_down);
-  a.w1 = nullptr;
-  a.act = reinterpret_cast<const __nv_bfloat16*>(ws + W.h);
-  a.out = ws + W.o;
-  a.weight = wts;
-  a.K = I;
-  a.N = H;
-  a.act_div = 1;
-  w4_gemv<W4_F32>(launch, dim3((H + 31) / 32, tiles), a);
-  if (const moe_status_t s = launched(); s != MOE_OK) return s;
-  launch(true, w4_combine_kernel, dim3((T * H + 255) / 256), dim3(256), 0,
-         reinterpret_cast<const float*>(ws + W.o), T, k, H, static_cast<__nv_bfloat16*>(y));
+  w4_by_form(T, group, flags & MOE_FLAG_W4_ZEROS, [&](auto nb, auto g32, auto zp) {
+    constexpr int NB = decltype(nb)::value;
+    launch(true, w4_moe_kernel<NB, decltype(g32)::value, decltype(zp)::value>, dim3(w4_slots(*d)),
+           dim3(W4S_THREADS), w4s_smem<NB>(), a);
+  });
   return launched();
 }
 
