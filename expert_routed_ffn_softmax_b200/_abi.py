@@ -81,7 +81,8 @@ SIGNATURES = {
     "moe_w4_pack": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_w4_quantize_weights": (_I, [_P, _I, _I, _I, _I, _U, _P, _P]),
     "moe_w4_dequantize_weights": (_I, [_P, _I, _I, _I, _I, _U, _P, _P]),
-    "moe_linear_w4": (_I, [_P, _P, _I, _I, _I, _I, _U, _P, _P]),
+    "moe_linear_w4_workspace_size": (_SZ, [_I, _I]),
+    "moe_linear_w4": (_I, [_P, _P, _I, _I, _I, _I, _U, _P, _P, _SZ, _P]),
     "moe_dense_w4_workspace_size": (_SZ, [_I, _I, _I]),
     "moe_dense_ffn_w4": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _U, _P, _P, _SZ, _P]),
     "moe_w4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _U]),
@@ -599,7 +600,7 @@ def w4_dequantize(w: W4Weights, out: torch.Tensor | None = None) -> torch.Tensor
 
 @_on_device
 def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None,
-              fp32: bool = False) -> torch.Tensor:
+              fp32: bool = False, workspace_buf: torch.Tensor | None = None) -> torch.Tensor:
     """moe_linear_w4: y = x W for x bf16 [T, K], T <= 16, and one 4-bit matrix -> y [T, N], bf16
     (or fp32 with fp32=True).  stream=: run on that stream."""
     if not isinstance(w, W4Weights):
@@ -617,9 +618,16 @@ def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None,
     else:
         py = _same(out, "out", dt, (T, w.N), dev)
     if T:
-        _check(load().moe_linear_w4(px, pw, T, K, w.N, w.group,
-                                    w.flags | (MOE_FLAG_F32_OUT if fp32 else 0), py,
-                                    _raw_stream(dev)), "moe_linear_w4")
+        L = load()
+        n = L.moe_linear_w4_workspace_size(T, K)
+        if n == 0:
+            pws = 0
+        else:
+            ws = _w4_workspace(n, workspace_buf, "", dev)
+            pws, n = ws.data_ptr(), ws.numel()
+        _check(L.moe_linear_w4(px, pw, T, K, w.N, w.group,
+                               w.flags | (MOE_FLAG_F32_OUT if fp32 else 0), py, pws, n,
+                               _raw_stream(dev)), "moe_linear_w4")
     return out
 
 

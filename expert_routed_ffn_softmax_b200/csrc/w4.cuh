@@ -219,7 +219,7 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 }
 
 // Decoding.  A pair of codes becomes a pair of exact bf16 values (code - zero) / 4 in one logical
-// operation and one fused multiply-add; the 4 goes into the group's scale.  The logical pipe is
+// operation and one fused multiply-add; the 4 is put back where the sums are joined.  The logical pipe is
 // the scarce one (half the issue rate), so the shifts are kept to one per eight codes:
 //   nibbles 0 and 4 of a word: OR with 0x4300 makes 128 + code (whose unit in the last place is
 //       1), times 1/4, minus (128 + zero) / 4;
@@ -275,13 +275,14 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
 
 // acc[i][j] += block i * activation fragments, for the records of NS strips at the same place
 // along K, in shared memory: rec[i] = the record's address + 16 lane.  x[j]: the address of the
-// lane's 8 activations of the first half (elements 8 t .. + 7 of row g + 8 j, for lane 4 g + t).
+// lane's 8 activations of the first half (elements 8 t .. + 7 of row g + 8 j, for lane 4 g + t);
+// those of the second half are x_half bytes on.
 // acc[i][j]: (row g, activation rows 8 j + 2 t and + 1), (row g + 8, the same).  The products of
 // a group are exact integers (over 4) times bf16, summed in fp32 by the matrix instruction; the
 // scale is applied once per group, in fp32, so nothing is rounded to bf16 on the way.
 template <int NS, int NB, bool G32, bool ZP>
 __device__ __forceinline__ void w4_block(float (&acc)[NS][NB][4], const uint32_t (&rec)[NS], int lane,
-                                         const uint32_t (&x)[NB]) {
+                                         const uint32_t (&x)[NB], uint32_t x_half) {
   constexpr int GPB = G32 ? 2 : 1;
   uint4 q[NS];
   uint32_t sc[NS], zp[NS];
@@ -296,7 +297,7 @@ __device__ __forceinline__ void w4_block(float (&acc)[NS][NB][4], const uint32_t
   for (int h = 0; h < 2; ++h) {
     uint4 xf[NB];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) xf[j] = h ? lds_v4<64>(x[j]) : lds_v4<0>(x[j]);
+    for (int j = 0; j < NB; ++j) xf[j] = lds_v4<0>(h ? x[j] + x_half : x[j]);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const uint32_t lo = h ? q[i].z : q[i].x, hi = h ? q[i].w : q[i].y;
@@ -318,8 +319,7 @@ __device__ __forceinline__ void w4_block(float (&acc)[NS][NB][4], const uint32_t
       }
       if (G32 || h == 1) {
         const uint32_t s2 = G32 && h ? lds_u32<512 + 32>(sc[i]) : lds_u32<512>(sc[i]);
-        const float s_lo = 4.f * __uint_as_float(s2 << 16);
-        const float s_hi = 4.f * __uint_as_float(s2 & 0xffff0000u);
+        const float s_lo = __uint_as_float(s2 << 16), s_hi = __uint_as_float(s2 & 0xffff0000u);
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           acc[i][j][0] = fmaf(s_lo, p[i][j][0], acc[i][j][0]);

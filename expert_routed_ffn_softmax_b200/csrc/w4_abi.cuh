@@ -30,37 +30,84 @@ auto w4_by_form(int T, int group, bool zeros, F&& fn) {
 // CTAs of the streaming kernels that run at once.
 int w4_slots(const DeviceState& d) { return 2 * std::max(1, d.num_sms); }
 
-// log2 of the row groups (of two strips) per unit of a linear layer.  A taller unit reads the
-// activations less often and joins fewer partial sums; a lower one deals out more evenly.  The
-// cost of a choice is its rounds of units over the CTAs, each the unit's weight and activation
-// bytes plus what a unit costs apart from them, in bytes.
-int w4_row_groups(int T, int K, int N, int record, int slots) {
-  int best = 0;
+// How a linear layer (or the gate | up half of a GEGLU MLP) is cut.  A CTA keeps the activations
+// in shared memory for all of its units where they fit beside a ring of 3 x 16 KB (T K <= 22 K
+// elements, say); longer ones come as fragments with each chunk of weights, so a taller unit reads
+// them less often, while a lower one deals out more evenly.  The cost of a choice is the time of
+// its fullest SM, in bytes at the memory's rate: its units' weights and activations, or the copies
+// that bring them (one is issued in about 0.1 us), and what a unit costs apart from that.
+struct W4Plan {
+  int lg = 0, units = 0, step = 0, stage = 0, smem = 0, frag = 0;
+};
+// Whether activations [T][K] come as fragments.
+template <int NB> bool w4_frag(int T, int K) {
+  return NB == 2 || w4_linear_smem<NB>(T, K, 0, 16384).total > W4S_SMEM;
+}
+template <int NB>
+W4Plan w4_plan(int mode, int T, int K, int N, int record, int sms) {
+  W4Plan best;
+  best.frag = w4_frag<NB>(T, K);
+  const int kb = K / W4_KB, rest = w4_linear_smem<NB>(T, K, best.frag, 0).total;
+  const int room = std::min((W4S_SMEM - rest) / W4S_STAGES / 128 * 128, 30720);
   double least = 0;
   for (int lg = 0; lg < 4; ++lg) {
-    const int tall = 2 << lg, units = (N / W4_ROWS + tall - 1) / tall;
-    const double cost =
-        (units + slots - 1) / slots * ((double)tall * (K / W4_KB) * record + 2.0 * T * K + 6144.0);
-    if (lg == 0 || cost < least) {
+    const int strips = 2 << lg, per = mode == W4_GEGLU ? 1 << lg : strips;
+    const int block = strips * record + (best.frag ? w4_frag_block<NB>() : 0);
+    if (room < block) break;
+    W4Plan p = best;
+    p.lg = lg;
+    p.units = (N / W4_ROWS + per - 1) / per;
+    const int chunks = (kb + room / block - 1) / (room / block);
+    p.step = (kb + chunks - 1) / chunks;
+    p.stage = (p.step * block + 127) / 128 * 128;
+    p.smem = w4_linear_smem<NB>(T, K, p.frag, p.stage).total;
+    const int beside = p.units <= sms ? 1 : 2;   // CTAs of an SM
+    const double unit = std::max((double)kb * block, 2400.0 * chunks * (strips + p.frag)) + 8192;
+    // units an SM's CTAs run one after the other; stolen units even out the last round
+    const double rounds = p.units <= 2 * sms ? 1.0 : (double)p.units / (2 * sms) + 0.5;
+    const double cost = beside * rounds * unit;
+    if (least == 0 || cost < least) {
       least = cost;
-      best = lg;
+      best = p;
     }
   }
   return best;
 }
 
-// One linear layer (or the gate | up half of a GEGLU MLP) on the streaming kernel.
 template <int MODE>
-moe_status_t w4_stream(const Launch& launch, const DeviceState& d, W4Linear a, int group, bool zeros) {
-  const int slots = w4_slots(d);
-  a.lg = MODE == W4_GEGLU ? 0 : w4_row_groups(a.T, a.K, a.N, w4_record(group, zeros), slots);
-  a.units = MODE == W4_GEGLU ? a.N / W4_ROWS : (a.N / W4_ROWS + (2 << a.lg) - 1) >> (a.lg + 1);
+moe_status_t w4_stream(cudaStream_t st, const DeviceState& d, W4Linear a, int group, bool zeros) {
   w4_by_form(a.T, group, zeros, [&](auto nb, auto g32, auto zp) {
     constexpr int NB = decltype(nb)::value;
-    launch(true, w4_linear_kernel<NB, decltype(g32)::value, decltype(zp)::value, MODE>,
-           dim3(std::min(a.units, slots)), dim3(W4S_THREADS), w4s_smem<NB>(), a);
+    const int sms = std::max(1, d.num_sms);
+    const W4Plan p = w4_plan<NB>(MODE, a.T, a.K, a.N, w4_record(group, zeros), sms);
+    a.lg = p.lg;
+    a.units = p.units;
+    a.step = p.step;
+    a.stage = p.stage;
+    a.frag = p.frag;
+    a.steal = p.units > 2 * sms;
+    const Launch launch{st, true};
+    launch(true, w4_linear_kernel<NB, decltype(g32)::value, decltype(zp)::value, MODE>, dim3(p.units),
+           dim3(W4S_THREADS), p.smem, a);
   });
   return launched();
+}
+
+// Activations x [T][K] for w4_stream: x itself, or its fragments in `scratch` (one launch more,
+// after which the stream may start its weights early).
+bool w4_needs_fragments(int T, int K) { return T > 8 ? w4_frag<2>(T, K) : w4_frag<1>(T, K); }
+size_t w4_fragment_bytes(int T, int K) {
+  return w4_needs_fragments(T, K) ? align256((size_t)(K / W4_KB) * (T > 8 ? w4_frag_block<2>() : w4_frag_block<1>()))
+                                  : 0;
+}
+void w4_activations(cudaStream_t st, const void* x, void* scratch, W4Linear& a) {
+  a.act = static_cast<const __nv_bfloat16*>(x);
+  if (!w4_needs_fragments(a.T, a.K)) return;
+  const Launch launch{st, true};
+  launch(true, w4_fragment_kernel, dim3((a.T * a.K / 8 + 255) / 256), dim3(256), 0, a.act, a.T, a.K,
+         a.T > 8 ? 2 : 1, static_cast<__nv_bfloat16*>(scratch));
+  a.act = static_cast<const __nv_bfloat16*>(scratch);
+  a.early = 1;
 }
 
 // Shared memory limits of the streaming kernels, once per device.
@@ -72,7 +119,7 @@ bool w4_linear_attrs() {
       constexpr int NB = decltype(nb)::value;
       ok = ok && cudaFuncSetAttribute(w4_linear_kernel<NB, decltype(g32)::value, decltype(zp)::value, MODE>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      w4s_smem<NB>()) == cudaSuccess;
+                                      W4S_SMEM) == cudaSuccess;
     });
   return ok;
 }
@@ -83,7 +130,7 @@ bool w4_moe_attrs() {
       constexpr int NB = decltype(nb)::value;
       ok = ok && cudaFuncSetAttribute(w4_moe_kernel<NB, decltype(g32)::value, decltype(zp)::value>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      w4s_smem<NB>()) == cudaSuccess;
+                                      W4S_SMEM) == cudaSuccess;
     });
   return ok;
 }
@@ -120,12 +167,12 @@ W4Layout w4_layout(int T, int H, int E, int I, int k) {
   };
   const size_t P = (size_t)T * k;
   L.slices = H / W4M_SLICE;
-  // W_down units of 128 rows
-  L.lg2 = 2;
+  // W_down units of 64 rows: at the layer's I = 704 their four copies are a chunk of 24 KB
+  L.lg2 = 1;
   L.n_ctr = W4M_CTR_O + H / W4_ROWS;
   L.logit = take(sizeof(double) * L.slices * T * E);
   L.xn2 = take(sizeof(double) * L.slices * T);
-  L.wn2 = take(sizeof(double) * L.slices * E);
+  L.wn2 = take(sizeof(double) * L.slices * (W4M_FRONT_THREADS / 32));
   L.stats = take(5 * sizeof(unsigned));
   L.ids = take(sizeof(int32_t) * P);
   L.wts = take(sizeof(float) * P);
@@ -201,35 +248,45 @@ moe_status_t moe_w4_dequantize_weights(const void* packed, int E, int K, int N, 
   return launched();
 }
 
+size_t moe_linear_w4_workspace_size(int T, int K) {
+  if (T < 1 || T > W4_MAX_T || !w4_matrix_ok(K, 16)) return 0;
+  return w4_fragment_bytes(T, K);
+}
+
 moe_status_t moe_linear_w4(const void* x, const void* w, int T, int K, int N, int group,
-                           unsigned flags, void* y, void* stream) {
+                           unsigned flags, void* y, void* workspace, size_t workspace_bytes,
+                           void* stream) {
   if (T < 0 || K <= 0 || N <= 0 || !w4_group_ok(group) ||
       (flags & ~(MOE_FLAG_W4_ZEROS | MOE_FLAG_F32_OUT)))
     return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || x == y)
+  if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(workspace) || x == y)
     return MOE_ERR_INVALID_ARG;
   if (T > W4_MAX_T || !w4_matrix_ok(K, N)) return MOE_ERR_UNSUPPORTED;
+  const size_t need = w4_fragment_bytes(T, K);
+  if (need && !workspace) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MOE_ERR_NO_WORKSPACE;
   int dev = 0;
   DeviceState* d = w4_device_state(&dev);
   if (!d) return MOE_ERR_CUDA;
   t_kernels = 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   W4Linear a = {};
   a.w0 = static_cast<const uint8_t*>(w);
-  a.act = static_cast<const __nv_bfloat16*>(x);
   a.out = y;
   a.T = T;
   a.K = K;
   a.N = N;
+  w4_activations(st, x, workspace, a);
   const bool zeros = flags & MOE_FLAG_W4_ZEROS;
-  const Launch launch{static_cast<cudaStream_t>(stream), true};
-  return (flags & MOE_FLAG_F32_OUT) ? w4_stream<W4_LINEAR_F32>(launch, *d, a, group, zeros)
-                                    : w4_stream<W4_LINEAR>(launch, *d, a, group, zeros);
+  return (flags & MOE_FLAG_F32_OUT) ? w4_stream<W4_LINEAR_F32>(st, *d, a, group, zeros)
+                                    : w4_stream<W4_LINEAR>(st, *d, a, group, zeros);
 }
 
+// Workspace of the dense MLP: h (rows, or fragments), then the fragments of x.
 size_t moe_dense_w4_workspace_size(int T, int H, int I) {
   if (T < 1 || T > W4_MAX_T || H < 64 || H > 16384 || H % 64 || I < 64 || I > 8192 || I % 64) return 0;
-  return align256(2 * (size_t)T * I);   // h
+  return std::max(align256(2 * (size_t)T * I), w4_fragment_bytes(T, I)) + w4_fragment_bytes(T, H);
 }
 
 moe_status_t moe_dense_ffn_w4(const void* x, const void* w_gate, const void* w_up, const void* w_down,
@@ -242,32 +299,33 @@ moe_status_t moe_dense_ffn_w4(const void* x, const void* w_gate, const void* w_u
   if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) ||
       !aligned16(y) || !aligned16(workspace) || x == y)
     return MOE_ERR_INVALID_ARG;
-  if (moe_dense_w4_workspace_size(T, H, I) == 0) return MOE_ERR_UNSUPPORTED;
-  if (workspace_bytes < moe_dense_w4_workspace_size(T, H, I)) return MOE_ERR_NO_WORKSPACE;
+  const size_t need = moe_dense_w4_workspace_size(T, H, I);
+  if (need == 0) return MOE_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return MOE_ERR_NO_WORKSPACE;
   int dev = 0;
   DeviceState* d = w4_device_state(&dev);
   if (!d) return MOE_ERR_CUDA;
   t_kernels = 0;
-  const Launch launch{static_cast<cudaStream_t>(stream), true};
-  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool zeros = flags & MOE_FLAG_W4_ZEROS;
   W4Linear a = {};
   a.w0 = static_cast<const uint8_t*>(w_gate);
   a.w1 = static_cast<const uint8_t*>(w_up);
-  a.act = static_cast<const __nv_bfloat16*>(x);
-  a.out = h;
+  a.out = workspace;
   a.T = T;
   a.K = H;
   a.N = I;
-  if (const moe_status_t s = w4_stream<W4_GEGLU>(launch, *d, a, group, zeros); s != MOE_OK) return s;
+  a.out_frag = w4_needs_fragments(T, I) ? (T > 8 ? 2 : 1) : 0;
+  w4_activations(st, x, static_cast<uint8_t*>(workspace) + need - w4_fragment_bytes(T, H), a);
+  if (const moe_status_t s = w4_stream<W4_GEGLU>(st, *d, a, group, zeros); s != MOE_OK) return s;
   a.w0 = static_cast<const uint8_t*>(w_down);
   a.w1 = nullptr;
-  a.act = h;
+  a.act = static_cast<const __nv_bfloat16*>(workspace);
   a.out = y;
   a.K = I;
   a.N = H;
   a.early = 1;
-  return w4_stream<W4_LINEAR>(launch, *d, a, group, zeros);
+  return w4_stream<W4_LINEAR>(st, *d, a, group, zeros);
 }
 
 size_t moe_w4_workspace_size(int T, int H, int E, int I, int k, unsigned flags) {
@@ -330,18 +388,13 @@ moe_status_t moe_forward_w4(const void* x, const void* w_router, const float* ro
   a.o = reinterpret_cast<float*>(ws + W.o);
   a.y = static_cast<__nv_bfloat16*>(y);
   const Launch launch{static_cast<cudaStream_t>(stream), true};
-  auto front = [&](auto kernel) {
-    launch(true, kernel, dim3(W.slices), dim3(W4M_FRONT_THREADS), 0, a.x, a.wr, T, H, E, logit, xn2, wn2,
-           a.ctr, W.n_ctr, a.stats);
-  };
-  if (T <= 2) front(w4_front_kernel<2>);
-  else if (T <= 8) front(w4_front_kernel<8>);
-  else front(w4_front_kernel<16>);
+  launch(true, w4_front_kernel, dim3(W.slices, (T + W4M_TT - 1) / W4M_TT), dim3(W4M_FRONT_THREADS), 0, a.x,
+         a.wr, T, H, E, logit, xn2, wn2, a.ctr, W.n_ctr, a.stats);
   if (const moe_status_t s = launched(); s != MOE_OK) return s;
   w4_by_form(T, group, flags & MOE_FLAG_W4_ZEROS, [&](auto nb, auto g32, auto zp) {
     constexpr int NB = decltype(nb)::value;
     launch(true, w4_moe_kernel<NB, decltype(g32)::value, decltype(zp)::value>, dim3(w4_slots(*d)),
-           dim3(W4S_THREADS), w4s_smem<NB>(), a);
+           dim3(W4S_THREADS), W4S_SMEM, a);
   });
   return launched();
 }

@@ -25,90 +25,101 @@ constexpr int W4M_FRONT_THREADS = 256;
 constexpr int W4M_MAX_PAIRS = 128;
 
 // ----------------------------------------------------------------------------- partial logits
-// part_logit [S][T][E], part_xn2 [S][T], part_wn2 [S][E] over slice blockIdx.x.  Thread = two
-// experts x every n-th row of the slice, all tokens (TT >= T of them); its rows' weights are
-// loaded before any is used.  Every product is exact in fp64.
-template <int TT>
+// part_logit [S][T][E], part_xn2 [S][T] and part_wn2 [S][warps] over slice blockIdx.x, for the
+// tokens of group blockIdx.y.  Thread = two experts x every n-th row of the slice, W4M_TT tokens;
+// its rows' weights are loaded before any is used.  Every product is exact in fp64.  part_wn2:
+// per warp a bound of its columns' parts of |w_e|^2, so that the sum over slices and warps bounds
+// every column's squared norm (the rounding bound needs no more, and 8 numbers a slice are read
+// instead of E).
+constexpr int W4M_TT = 4;
 __global__ void __launch_bounds__(W4M_FRONT_THREADS) w4_front_kernel(
     const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wr, int T, int H, int E,
     double* __restrict__ part_logit, double* __restrict__ part_xn2, double* __restrict__ part_wn2,
     int* __restrict__ counters, int n_counters, unsigned* __restrict__ stats) {
+  constexpr int TT = W4M_TT;
   pdl_wait();
   pdl_trigger();
   __shared__ double xs[W4M_SLICE][TT];
-  __shared__ double red[W4M_FRONT_THREADS][6];
-  const int tid = threadIdx.x, s = blockIdx.x, h0 = s * W4M_SLICE;
-  for (int i = s * W4M_FRONT_THREADS + tid; i < n_counters; i += gridDim.x * W4M_FRONT_THREADS)
-    counters[i] = 0;
-  if (s == 0 && tid < 5) stats[tid] = 0;
+  __shared__ double red[2 * TT][W4M_FRONT_THREADS];
+  const int tid = threadIdx.x, s = blockIdx.x, h0 = s * W4M_SLICE, t0 = blockIdx.y * TT;
+  const int nt = min(TT, T - t0);
+  if (blockIdx.y == 0) {
+    for (int i = s * W4M_FRONT_THREADS + tid; i < n_counters; i += gridDim.x * W4M_FRONT_THREADS)
+      counters[i] = 0;
+    if (s == 0 && tid < 5) stats[tid] = 0;
+  }
   const int pairs = E / 2, groups = W4M_FRONT_THREADS / pairs;   // E % 4 == 0, E <= 256
   const int ep = tid % pairs, grp = tid / pairs;
   const bool active = grp < groups;
-  constexpr int MAXR = 32;   // rows of a thread loaded at once
-  uint32_t w[MAXR];
   const __nv_bfloat16* wp = wr + (size_t)h0 * E + 2 * ep;
+  constexpr int BATCH = 16;   // rows of a thread loaded at once
+  uint32_t w[BATCH];
+  auto load = [&](int i0) {
 #pragma unroll
-  for (int i = 0; i < MAXR; ++i) {
-    const int h = grp + i * groups;
-    w[i] = active && h < W4M_SLICE ? __ldg(reinterpret_cast<const unsigned*>(wp + (size_t)h * E)) : 0u;
-  }
-  for (int i = tid; i < W4M_SLICE * TT; i += W4M_FRONT_THREADS) {
-    const int t = i / W4M_SLICE, h = i % W4M_SLICE;
-    xs[h][t] = t < T ? (double)__bfloat162float(x[(size_t)t * H + h0 + h]) : 0.0;
+    for (int i = 0; i < BATCH; ++i) {
+      const int h = grp + (i0 + i) * groups;
+      w[i] = active && h < W4M_SLICE ? __ldg(reinterpret_cast<const unsigned*>(wp + (size_t)h * E)) : 0u;
+    }
+  };
+  load(0);
+  {
+    const int t = tid / W4M_SLICE, h = tid % W4M_SLICE;   // 4 tokens x 64 rows = one element a thread
+    xs[h][t] = t < nt ? (double)__bfloat162float(x[(size_t)(t0 + t) * H + h0 + h]) : 0.0;
   }
   __syncthreads();
   double acc[TT][2], wn[2] = {0.0, 0.0};
 #pragma unroll
   for (int t = 0; t < TT; ++t) acc[t][0] = acc[t][1] = 0.0;
-  if (active) {
+  for (int i0 = 0;;) {
 #pragma unroll
-    for (int i = 0; i < MAXR; ++i) {
-      const int h = grp + i * groups;
-      if (h < W4M_SLICE) {
-        const double w0 = (double)__uint_as_float(w[i] << 16);
-        const double w1 = (double)__uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < BATCH; ++i) {
+      const int h = min(grp + (i0 + i) * groups, W4M_SLICE - 1);   // rows past the end hold zeros
+      const double w0 = (double)__uint_as_float(w[i] << 16);
+      const double w1 = (double)__uint_as_float(w[i] & 0xffff0000u);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const double xv = xs[h][t];
-          acc[t][0] = fma(xv, w0, acc[t][0]);
-          acc[t][1] = fma(xv, w1, acc[t][1]);
-        }
-        wn[0] = fma(w0, w0, wn[0]);
-        wn[1] = fma(w1, w1, wn[1]);
+      for (int t = 0; t < TT; ++t) {
+        const double xv = xs[h][t];
+        acc[t][0] = fma(xv, w0, acc[t][0]);
+        acc[t][1] = fma(xv, w1, acc[t][1]);
       }
+      wn[0] = fma(w0, w0, wn[0]);
+      wn[1] = fma(w1, w1, wn[1]);
     }
+    i0 += BATCH;
+    if (i0 * groups >= W4M_SLICE) break;
+    load(i0);
   }
-  // join the row groups, two tokens (or one, and the norms) at a time, in group order
 #pragma unroll
-  for (int t = 0; t <= TT; t += 2) {
-    __syncthreads();
-    if (t < TT) {
-      red[tid][0] = acc[t < TT ? t : 0][0];
-      red[tid][1] = acc[t < TT ? t : 0][1];
-      red[tid][2] = acc[t + 1 < TT ? t + 1 : 0][0];
-      red[tid][3] = acc[t + 1 < TT ? t + 1 : 0][1];
-    } else {
-      red[tid][0] = wn[0];
-      red[tid][1] = wn[1];
-    }
-    __syncthreads();
-    for (int i = tid; i < 2 * E; i += W4M_FRONT_THREADS) {
-      const int u = i / E, e = i - u * E;
-      double v = 0.0;
-      for (int g = 0; g < groups; ++g) v += red[g * pairs + e / 2][2 * u + (e & 1)];
-      if (t < TT) {
-        if (t + u < T) part_logit[((size_t)s * T + t + u) * E + e] = v;
-      } else if (u == 0) {
-        part_wn2[(size_t)s * E + e] = v;
-      }
-    }
+  for (int t = 0; t < TT; ++t) {
+    red[2 * t][tid] = acc[t][0];
+    red[2 * t + 1][tid] = acc[t][1];
   }
-  if (tid < T) {
+  if (blockIdx.y == 0) {
+    double m = fmax(wn[0], wn[1]);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, off));
+    // with fewer than 32 pairs several parts of a column lie in one warp
+    if ((tid & 31) == 0)
+      part_wn2[s * (W4M_FRONT_THREADS / 32) + tid / 32] = pairs < 32 ? m * (32 / pairs + 1) : m;
+  }
+  __syncthreads();
+  // join the row groups, in group order
+  for (int i = tid; i < nt * E; i += W4M_FRONT_THREADS) {
+    const int t = i / E, e = i - t * E;
     double v = 0.0;
-    for (int h = 0; h < W4M_SLICE; ++h) v = fma(xs[h][tid], xs[h][tid], v);
-    part_xn2[(size_t)s * T + tid] = v;
+    for (int g = 0; g < groups; ++g) v += red[2 * t + (e & 1)][g * pairs + e / 2];
+    part_logit[((size_t)s * T + t0 + t) * E + e] = v;
+  }
+  if (tid / 32 < nt) {
+    const int t = tid / 32, lane = tid & 31;
+    double v = xs[lane][t] * xs[lane][t];
+    v = fma(xs[lane + 32][t], xs[lane + 32][t], v);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0) part_xn2[(size_t)s * T + t0 + t] = v;
   }
 }
+static_assert(W4M_TT * W4M_SLICE == W4M_FRONT_THREADS, "one activation per thread");
 
 // ----------------------------------------------------------------------------- the layer
 struct W4Moe {
@@ -123,14 +134,28 @@ struct W4Moe {
   float* wts;
   unsigned* stats;
   int32_t *counts, *offsets, *perm; // optional outputs
-  // counters, zeroed by the front kernel: {next token to select, tokens selected, next unit, -},
+  // counters, zeroed by the front kernel: {next token to select, tokens with ids, next unit, tokens
+  // with weights, GEMM-1 units joined (x joining warps)},
   // h_ready [128] per active expert, o_ready [row blocks of W_down]
   int* ctr;
   __nv_bfloat16* h;                 // [T k][I]
-  float* o;                         // [T k][H]: weighted expert outputs
+  float* o;                         // [T k][H]: expert outputs
   __nv_bfloat16* y;
 };
-constexpr int W4M_CTR_H = 4, W4M_CTR_O = W4M_CTR_H + W4M_MAX_PAIRS;
+constexpr int W4M_CTR_H = 8, W4M_CTR_O = W4M_CTR_H + W4M_MAX_PAIRS;
+
+// Wait until *p >= target (another CTA's release), polling without a pause: these hand-overs are
+// on the layer's critical path.
+__device__ __forceinline__ bool w4m_wait(const int* p, int target) {
+  if (ld_acquire_gpu(p) >= target) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (ld_acquire_gpu(p) < target)
+    if (global_timer_ns() - t0 > *reinterpret_cast<volatile unsigned long long*>(&g_wait_limit_ns)) {
+      raise_error(MOE_DEVERR_TIMEOUT);
+      return false;
+    }
+  return true;
+}
 
 // The exact recomputation of a token whose decisions the bounds cannot settle (rare; kept out of
 // line so that it does not cost the kernel registers).
@@ -147,68 +172,77 @@ __device__ __noinline__ void w4_exact_token(const double* sL, const double* sB, 
   router_finish_token<8>(L, B, t, a.x, a.wr, a.bias, a.H, a.E, a.k, a.renorm, a.ids, a.wts, a.stats, scratch);
 }
 
-// Select token t with the whole CTA.  scratch: at least 16 KB, 16-byte aligned.
+// Select token t with the whole CTA.  scratch: at least 16 KB, 16-byte aligned.  Each launch runs
+// this code cold (T CTAs, once), so it is kept short: integer keys for the ranking instead of
+// fp64 comparisons, few unrolled loops.
 __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratch) {
-  const int tid = threadIdx.x, lane = tid & 31, E = a.E;
-  double* sL = reinterpret_cast<double*>(scratch);   // [256] logits
+  constexpr int WARPS = W4S_THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
+  double* sL = reinterpret_cast<double*>(scratch);   // [256] logits (-inf past E)
   double* sB = sL + 256;                             // [256] rounding bounds
   double* sSelV = sB + 256;                          // [8]
   double* sSelB = sSelV + 8;                         // [8]
   int* sSelE = reinterpret_cast<int*>(sSelB + 8);    // [8]
-  double* sXn = sSelB + 16;                          // [1]
-  double* sPart = sSelB + 24;                        // [W4S_THREADS][2]
-  int* sRank = reinterpret_cast<int*>(sPart + 2 * W4S_THREADS);   // [256]
+  double* sNorm = sSelB + 16;                        // [2] |x_t|^2, bound of |w_e|^2
+  double* sPart = sSelB + 24;                        // [W4S_THREADS]
+  unsigned long long* sKey = reinterpret_cast<unsigned long long*>(sPart + W4S_THREADS);   // [256]
+  int* sRank = reinterpret_cast<int*>(sKey + 256);            // [256]
   const int groups = W4S_THREADS / E, e = tid % E, grp = tid / E;
   // the slices' partial sums: each group of threads adds every groups-th slice
   if (grp < groups) {
-    double v = 0.0, w2 = 0.0;
-    const double* p = a.part_logit + (size_t)t * E + e;
-    const size_t step = (size_t)a.T * E;
-#pragma unroll 8
-    for (int s = grp; s < a.slices; s += groups) {
-      v += __ldcg(p + s * step);
-      w2 += __ldcg(a.part_wn2 + (size_t)s * E + e);
-    }
-    sPart[2 * tid] = v;
-    sPart[2 * tid + 1] = w2;
-  }
-  if (tid >= W4S_THREADS - 32) {
     double v = 0.0;
-    for (int s = lane; s < a.slices; s += 32) v += __ldcg(a.part_xn2 + (size_t)s * a.T + t);
+    const double* p = a.part_logit + ((size_t)grp * a.T + t) * E + e;
+    const size_t step = (size_t)groups * a.T * E;
+    const int n = (a.slices - grp + groups - 1) / groups;
+    for (int s = 0; s < n; s += 24) {
+      double q[24];
+#pragma unroll
+      for (int i = 0; i < 24; ++i) q[i] = s + i < n ? __ldcg(p + (s + i) * step) : 0.0;
+#pragma unroll
+      for (int i = 0; i < 24; ++i) v += q[i];
+    }
+    sPart[tid] = v;
+  }
+  if (warp >= WARPS - 2) {
+    // the last two warps also add the norms
+    const bool xn = warp == WARPS - 1;
+    const int n = xn ? a.slices : a.slices * (W4M_FRONT_THREADS / 32);
+    double v = 0.0;
+#pragma unroll 8
+    for (int s = lane; s < n; s += 32) v += __ldcg(xn ? a.part_xn2 + (size_t)s * a.T + t : a.part_wn2 + s);
 #pragma unroll
     for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (lane == 0) *sXn = v;
+    if (lane == 0) sNorm[xn ? 0 : 1] = v;
   }
-  if (tid < 256) sRank[tid] = 0;
   __syncthreads();
   if (tid < E) {
-    double v = 0.0, w2 = 0.0;
-    for (int g = 0; g < groups; ++g) {
-      v += sPart[2 * (g * E + tid)];
-      w2 += sPart[2 * (g * E + tid) + 1];
-    }
+    double v = 0.0;
+    for (int g = 0; g < groups; ++g) v += sPart[g * E + tid];
     const double b = a.bias ? (double)a.bias[tid] : 0.0;
     if (a.bias) v += b;
     sL[tid] = v;
-    sB[tid] = a.beta_scale * (sqrt(*sXn * w2) * (1.0 + 1e-6) + fabs(b));
+    sB[tid] = a.beta_scale * (sqrt(sNorm[0] * sNorm[1]) * (1.0 + 1e-6) + fabs(b));
+    // an unsigned key in the logits' order (-0 as 0, NaN below every number)
+    const long long bits = __double_as_longlong(v + 0.0);
+    sKey[tid] = isnan(v) ? 1ull : (unsigned long long)(bits ^ ((bits >> 63) | (1ll << 63)));
+    sRank[tid] = 0;
   }
   __syncthreads();
-  // rank of expert e by (logit desc, id asc); NaN ranks below every number
+  // rank of expert e by (logit desc, id asc): each group of threads counts over a part of the ids
   if (grp < groups) {
-    const double ve = isnan(sL[e]) ? -INFINITY : sL[e];
+    const unsigned long long mine = sKey[e];
+    const int lo = grp * E / groups, hi = (grp + 1) * E / groups;
     int r = 0;
 #pragma unroll 4
-    for (int e2 = grp; e2 < E; e2 += groups) {
-      const double v2 = sL[e2];
-      r += rank_before(isnan(v2) ? -INFINITY : v2, e2, ve, e) ? 1 : 0;
-    }
+    for (int x = lo; x < hi; ++x) r += sKey[x] > mine - (x < e ? 1 : 0);
     if (r) atomicAdd(&sRank[e], r);
   }
   __syncthreads();
   if (tid < E && sRank[tid] < a.k) {
-    sSelE[sRank[tid]] = tid;
-    sSelV[sRank[tid]] = sL[tid];
-    sSelB[sRank[tid]] = sB[tid];
+    const int r = sRank[tid];
+    sSelE[r] = tid;
+    sSelV[r] = sL[tid];
+    sSelB[r] = sB[tid];
   }
   __syncthreads();
   // every decision must hold under the rounding bounds (as in router_finish_token)
@@ -219,26 +253,30 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
   if (tid < 32) {
     if (!ok) {
       w4_exact_token(sL, sB, t, a, sPart);
+      __syncwarp();
+      if (lane == 0) red_release_add_gpu(a.ctr + 1, 1);
     } else {
+      // the ids at once, for the CTAs that wait to stream; the weights are needed last
+      if (lane < a.k) a.ids[(size_t)t * a.k + lane] = sSelE[lane];
+      __syncwarp();
+      if (lane == 0) red_release_add_gpu(a.ctr + 1, 1);
+      // The differences are taken in fp64; their exponentials and the sum in fp32 (the weights are
+      // fp32: off by 2^-24 |difference| plus a few 2^-24).  The fp64 exp's code alone, fetched
+      // cold once a launch, took 3 us.
       const double m = sSelV[0];
-      const double ex = lane < a.k ? exp(sSelV[lane] - m) : 0.0;
-      double denom = 0.0;
-      if (a.renorm) {
-        for (int r = 0; r < a.k; ++r) denom += __shfl_sync(0xffffffffu, ex, r);
-      } else {
-        double sum = 0.0;
-        for (int i = lane; i < E; i += 32) sum += exp(sL[i] - m);
+      const float ex = lane < a.k ? expf((float)(sSelV[lane] - m)) : 0.f;
+      float sum = ex;
+      if (!a.renorm) {
+        sum = 0.f;
+#pragma unroll 1
+        for (int i = lane; i < E; i += 32) sum += expf((float)(sL[i] - m));
+      }
 #pragma unroll
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        denom = sum;
-      }
-      if (lane < a.k) {
-        a.ids[(size_t)t * a.k + lane] = sSelE[lane];
-        a.wts[(size_t)t * a.k + lane] = (float)(ex / denom);
-      }
+      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane < a.k) a.wts[(size_t)t * a.k + lane] = ex / sum;
     }
     __syncwarp();
-    if (lane == 0) red_release_add_gpu(a.ctr + 1, 1);
+    if (lane == 0) red_release_add_gpu(a.ctr + 3, 1);
   }
   __syncthreads();
 }
@@ -247,39 +285,63 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
 // ascending (the stable permutation of the dispatch).
 struct W4List {
   int* pair;    // [128] pairs in expert order
-  float* w;     // [128] their weights
+  int* step;    // [128] blocks per chunk of each active expert's units: gate | up, down (16 bits each)
   int* off;     // [129] first position of each active expert, and the end
   int* expert;  // [128] ids of the active experts
   int* info;    // {active experts}
 };
 
-__device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, int* sIds) {
+// sIds: scratch of W4M_MAX_PAIRS + 8 ints, 16-byte aligned.
+__device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, int* sIds, int stage,
+                                                int record) {
   const int tid = threadIdx.x, P = a.T * a.k;
-  int* sFirst = sIds + W4M_MAX_PAIRS;   // 1: the first pair of its expert
+  unsigned* sMask = reinterpret_cast<unsigned*>(sIds + W4M_MAX_PAIRS);   // active experts, one bit each
   const int id = tid < P ? __ldcg(a.ids + tid) : 0x7fffffff;
   if (tid < W4M_MAX_PAIRS) sIds[tid] = id;
-  if (tid == 0) *L.info = 0;
+  if (tid < 8) sMask[tid] = 0;
   __syncthreads();
   int before = 0, same = 0;
   if (tid < P) {
-    for (int q = 0; q < P; ++q) {
-      const int o = sIds[q];
-      before += o < id || (o == id && q < tid);
-      same += o == id && q < tid;
+    atomicOr(&sMask[id >> 5], 1u << (id & 31));
+#pragma unroll 4
+    for (int q = 0; q < P; q += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(sIds + q);
+      const int v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool eq = v[i] == id && q + i < tid;
+        same += eq;
+        before += eq || v[i] < id;
+      }
     }
-    sFirst[tid] = same == 0;
-    if (same == 0) atomicAdd(L.info, 1);
     L.pair[before] = tid;
-    L.w[before] = __ldcg(a.wts + tid);
   }
   __syncthreads();
+  int n = 0, at = 0;   // active experts, and those before this one
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const unsigned m = sMask[i];
+    n += __popc(m);
+    if (tid < P) at += i < id >> 5 ? __popc(m) : i == id >> 5 ? __popc(m & ((1u << (id & 31)) - 1)) : 0;
+  }
   if (tid < P && same == 0) {
-    int at = 0;
-    for (int q = 0; q < P; ++q) at += sFirst[q] && sIds[q] < id;
     L.expert[at] = id;
     L.off[at] = before;
   }
-  if (tid == 0) L.off[*L.info] = P;
+  if (tid == 0) {
+    L.off[n] = P;
+    *L.info = n;
+  }
+  __syncthreads();
+  if (tid < n) {
+    // blocks per chunk: as many as fit a stage, evened out over the unit
+    const int rows = L.off[tid + 1] - L.off[tid];
+    auto even = [&](int kb, int strips) {
+      const int most = (stage - 64 * rows) / (strips * record + 128 * rows), chunks = (kb + most - 1) / most;
+      return (kb + chunks - 1) / chunks;
+    };
+    L.step[tid] = even(a.H / W4_KB, 2) | even(a.I / W4_KB, 2 << a.lg2) << 16;
+  }
   __syncthreads();
 }
 
@@ -299,22 +361,46 @@ __device__ __forceinline__ void w4_write_aux(const W4Moe& a, const W4List& L, co
     for (int q = threadIdx.x; q < P; q += W4S_THREADS) a.perm[q] = L.pair[q];
 }
 
+// A unit, from the producer to the other roles; rewritten only after every multiply warp has
+// released a later unit's chunk (the ring holds at most W4S_STAGES chunks).
+struct __align__(16) W4Desc {
+  int unit;     // -1: no more work
+  int strips, rows, lg;
+  int blocks;   // along K
+  int step;     // blocks per chunk
+  int pad[2];
+};
+constexpr int W4M_DESCS = W4S_STAGES + 1;
+constexpr int W4M_LISTS = 4 * (4 + 4 * W4M_MAX_PAIRS + 4);
+template <int NB> __host__ __device__ constexpr int w4m_stage() {
+  return (W4S_SMEM - 2 * w4s_acc_bytes<NB>() - W4Sync::BYTES - (int)sizeof(W4Desc) * W4M_DESCS - 32 - W4M_LISTS) / 3 /
+         128 * 128;
+}
+
 template <int NB, bool G32, bool ZP>
 __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_constant__ W4Moe a) {
   constexpr int R = 512 + (G32 ? 2 : 1) * (ZP ? 48 : 32);
-  constexpr int S = W4Ring<NB>::STAGES;
+  constexpr int STAGE = w4m_stage<NB>();
   extern __shared__ __align__(128) uint8_t w4sm[];
-  const W4Smem L = w4s_layout<NB>(w4sm);
-  const W4Bars<NB> bar{L.bars};
+  uint8_t* at = w4sm + W4S_STAGES * STAGE;
+  float* acc_tiles = reinterpret_cast<float*>(at);
+  at += 2 * w4s_acc_bytes<NB>();
+  W4Desc* descs = reinterpret_cast<W4Desc*>(at);
+  at += sizeof(W4Desc) * W4M_DESCS;
+  int4* acc_unit = reinterpret_cast<int4*>(at);   // [2] {unit, strips, rows, lg}
+  at += 32;
+  W4Sync sy;
+  sy.init(at);
+  at += W4Sync::BYTES;
   W4List list;
-  list.info = L.list;
-  list.pair = L.list + 4;
-  list.w = reinterpret_cast<float*>(list.pair + W4M_MAX_PAIRS);
+  list.info = reinterpret_cast<int*>(at);
+  int* s_token = list.info + 1;
+  list.pair = list.info + 4;
+  list.step = list.pair + W4M_MAX_PAIRS;
   list.expert = list.pair + 2 * W4M_MAX_PAIRS;
   list.off = list.pair + 3 * W4M_MAX_PAIRS;
-  int* s_token = L.list + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) w4s_init<NB>(L);
+  if (tid == 0) sy.reset();
   pdl_wait();
   pdl_trigger();
   // ---- selection: tokens are taken from a counter until none is left (at once, when an earlier
@@ -331,12 +417,11 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
     if (t >= a.T) break;
     w4_select(a, t, w4sm);
   }
-  if (tid == 0) *s_token = !dead && wait_counter_geq(a.ctr + 1, a.T);
+  if (tid == 0) *s_token = !dead && w4m_wait(a.ctr + 1, a.T);
   __syncthreads();
   if (!*s_token) return;   // nothing is in flight
-  __threadfence();
-  int* sIds = reinterpret_cast<int*>(L.acc);   // scratch until the first unit is joined
-  w4_build_lists(a, list, sIds);
+  int* sIds = reinterpret_cast<int*>(acc_tiles);   // scratch until the first unit is joined
+  w4_build_lists(a, list, sIds, STAGE, R);
   if (blockIdx.x == 0 && (a.counts || a.offsets || a.perm)) {
     w4_write_aux(a, list, sIds);
     __syncthreads();
@@ -345,90 +430,189 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
   const int kb1 = a.H / W4_KB, kb2 = a.I / W4_KB, strips1 = a.I / W4_ROWS, strips2 = a.H / W4_ROWS;
   const int nb2 = (strips2 + (2 << a.lg2) - 1) >> (a.lg2 + 1);   // W_down row blocks
   const int U1 = n_act * strips1, units = U1 + n_act * nb2;
+  // v / per = umulhi(v, magic) for v * per < 2^32 (at most 128 * 512 * 1024... units)
+  const unsigned magic1 = 0xffffffffu / strips1 + 1, magic2 = 0xffffffffu / nb2 + 1;
+  auto split = [&](int c, bool& down, int& ai, int& blk) {
+    down = c >= U1;
+    const int v = down ? c - U1 : c, per = down ? nb2 : strips1;
+    ai = per == 1 ? v : (int)__umulhi((unsigned)v, down ? magic2 : magic1);
+    blk = v - ai * per;
+  };
   int* h_ready = a.ctr + W4M_CTR_H;
   int* o_ready = a.ctr + W4M_CTR_O;
 
   if (warp == W4S_MMA_WARPS + W4S_EPI_WARPS) {
-    fence_proxy_async_smem();   // the ring held generic writes (the selection's scratch)
-    fence_proxy_async_global();
-    W4Producer<NB, R> p{L, w4sm, lane};
-    bool ok = true;
-    int c = 0;
-    if (lane == 0) c = atomicAdd(a.ctr + 2, 1);
-    c = __shfl_sync(0xffffffffu, c, 0);
-    while (ok && c < units) {
-      int next = 0;
-      if (lane == 0) next = atomicAdd(a.ctr + 2, 1);   // one unit ahead
-      W4Unit un;
-      un.id = c;
-      const bool down = c >= U1;
-      const int v = down ? c - U1 : c, per = down ? nb2 : strips1, ai = v / per, b = v - ai * per;
-      const int off = list.off[ai], e = list.expert[ai];
-      un.rows = list.off[ai + 1] - off;
-      const int pair = list.pair[off + min(lane, un.rows - 1)];
-      const __nv_bfloat16* row;
-      if (!down) {
-        un.kb = kb1;
-        un.strips = 2;
-        un.lg = 0;
-        un.pitch = 0;
-        const size_t at = ((size_t)e * strips1 + b) * kb1 * R;
-        un.s0 = a.wg + at;
-        un.s1 = a.wu + at;
-        row = a.x + (size_t)(pair / a.k) * a.H;
-      } else {
-        un.kb = kb2;
-        const int s0 = b << (a.lg2 + 1);
-        un.strips = min(2 << a.lg2, strips2 - s0);
-        un.lg = a.lg2;
-        un.pitch = (size_t)kb2 * R;
-        un.s0 = a.wd + ((size_t)e * strips2 + s0) * un.pitch;
-        un.s1 = un.s0 + un.pitch;
-        row = a.h + (size_t)pair * a.I;
+    if (lane == 0) {
+      fence_proxy_async_smem();   // the ring held generic writes (the selection's scratch)
+      fence_proxy_async_global();
+      const uint32_t ring = smem_u32(w4sm);
+      W4Pos pos;
+      int q = 0, n_unit = 0;
+      bool ok = true, all_h = false;
+      // Wait for the next stage; false when the CTA gives up.
+      auto acquire = [&] {
+        if (sy.aborted() || (q >= W4S_STAGES && !w4s_wait(sy.empty(pos.s), pos.phase ^ 1))) return false;
+        sy.flags[1] = q + 1;
+        return true;
+      };
+      int c = atomicAdd(a.ctr + 2, 1);
+      while (ok && c < units) {
+        const int next = atomicAdd(a.ctr + 2, 1);   // one unit ahead
+        bool down;
+        int ai, blk;
+        split(c, down, ai, blk);
+        const int off = list.off[ai], rows = list.off[ai + 1] - off, e = list.expert[ai];
+        const int lg = down ? a.lg2 : 0, s0 = down ? blk << (lg + 1) : blk, kb = down ? kb2 : kb1;
+        const int strips = down ? min(2 << lg, strips2 - s0) : 2;
+        const size_t pitch = (size_t)kb * R;
+        const size_t w_at = ((size_t)e * (down ? strips2 : strips1) + s0) * pitch;
+        const int step = down ? list.step[ai] >> 16 : list.step[ai] & 0xffff;
+        int4* d = reinterpret_cast<int4*>(descs + n_unit % W4M_DESCS);
+        const int width = down ? a.I : a.H;
+        const __nv_bfloat16* act = down ? a.h : a.x;
+        // weights and activation rows of the chunk at block b, into stage s
+        auto weights = [&](int b, int s) {
+          const uint32_t bytes = min(step, kb - b) * R;
+          uint32_t dst = ring + s * STAGE;
+          mbar_arrive_expect_tx(sy.full(s), strips * bytes + rows * 128 * min(step, kb - b));
+          if (down) {
+            const uint8_t* src = a.wd + w_at + (size_t)b * R;
+            for (int i = 0; i < strips; ++i, src += pitch, dst += bytes) bulk_load(dst, src, bytes, sy.full(s));
+          } else {
+            bulk_load(dst, a.wg + w_at + (size_t)b * R, bytes, sy.full(s));
+            bulk_load(dst + bytes, a.wu + w_at + (size_t)b * R, bytes, sy.full(s));
+          }
+        };
+        auto activations = [&](int b, int s) {
+          const int n = min(step, kb - b);
+          uint32_t dst = ring + s * STAGE + strips * n * R;
+          for (int i = 0; i < rows; ++i, dst += 128 * n + 64) {
+            const int pair = list.pair[off + i];
+            bulk_load(dst, act + (size_t)(down ? pair : pair / a.k) * width + 64 * b, 128 * n, sy.full(s));
+          }
+        };
+        int b = 0;
+        if (down) {
+          // the first stages' weights, then wait for the expert's h, then its rows
+          const W4Pos from = pos;
+          int n = 0;
+          for (; n < W4S_STAGES && n * step < kb && ok; ++n) {
+            ok = acquire();
+            if (!ok) break;
+            if (n == 0) {
+              d[0] = make_int4(c, strips, rows, lg);
+              d[1] = make_int4(kb, step, 0, 0);
+            }
+            weights(n * step, pos.s);
+            ++q;
+            pos.next();
+          }
+          if (ok && !all_h) {
+            ok = w4m_wait(h_ready + ai, W4S_EPI_WARPS * strips1);
+            all_h = ld_acquire_gpu(a.ctr + 4) == W4S_EPI_WARPS * U1;
+          }
+          fence_proxy_async_global();
+          W4Pos p = from;
+          for (int i = 0; i < n && ok; ++i, p.next()) activations(i * step, p.s);
+          b = n * step;
+        }
+        for (; b < kb && ok; b += step) {
+          ok = acquire();
+          if (!ok) break;
+          if (b == 0) {
+            d[0] = make_int4(c, strips, rows, lg);
+            d[1] = make_int4(kb, step, 0, 0);
+          }
+          weights(b, pos.s);
+          activations(b, pos.s);
+          ++q;
+          pos.next();
+        }
+        ++n_unit;
+        c = next;
       }
-      const int step = w4s_chunk_blocks<NB, R>(un.kb, un.strips, un.rows);
-      int first = 0;
-      if (down) {
-        // the first stages' weights, then wait for the expert's h, then its rows
-        const int pre = min((un.kb + step - 1) / step, S);
-        for (int i = 0; i < pre && ok; ++i)
-          ok = p.weights(un, i * step, min(step, un.kb - i * step), p.q + i);
-        int ready = 1;
-        if (ok && lane == 0) ready = wait_counter_geq(h_ready + ai, W4S_EPI_WARPS * strips1);
-        ok = __shfl_sync(0xffffffffu, ready, 0) && ok;
-        fence_proxy_async_global();
-        for (int i = 0; i < pre && ok; ++i) p.rows(un, i * step, min(step, un.kb - i * step), p.q + i, row);
-        p.q += pre;
-        first = pre * step;
+      if (ok) {
+        ok = acquire();
+        descs[n_unit % W4M_DESCS].unit = -1;
+        if (ok) mbar_arrive(sy.full(pos.s));
       }
-      for (; first < un.kb && ok; first += step) {
-        const int n = min(step, un.kb - first);
-        ok = p.weights(un, first, n, p.q);
-        if (ok) p.rows(un, first, n, p.q, row);
-        ++p.q;
-      }
-      c = __shfl_sync(0xffffffffu, next, 0);
+      if (!ok) sy.abort();
     }
-    if (ok) ok = p.stop();
-    if (!ok) *reinterpret_cast<volatile int*>(L.abort_flag) = 1;
   } else if (warp < W4S_MMA_WARPS) {
-    w4s_multiply<NB, G32, ZP>(L, warp, lane);
+    const int g = lane >> 2, t = lane & 3;
+    float acc[2][NB][4];
+#pragma unroll
+    for (int i = 0; i < 2 * NB * 4; ++i) acc[i / (4 * NB)][i / 4 % NB][i % 4] = 0.f;
+    W4Pos pos;
+    int q = 0;
+    bool ok = true;
+    for (int n_unit = 0;; ++n_unit) {
+      if (sy.aborted() || !w4s_wait(sy.full(pos.s), pos.phase)) {
+        ok = false;
+        break;
+      }
+      const uint32_t head = smem_u32(descs + n_unit % W4M_DESCS);
+      const uint4 d0 = lds_v4<0>(head), d1 = lds_v4<16>(head);
+      const int unit = (int)d0.x, strips = d0.y, rows = d0.z, lg = d0.w, kb = d1.x, step = d1.y;
+      const int slices = W4S_MMA_WARPS >> lg, group = warp & ((1 << lg) - 1), slice = warp >> lg;
+      for (int b = 0; unit >= 0 && b < kb; b += step) {
+        if (b && !w4s_wait(sy.full(pos.s), pos.phase)) {
+          ok = false;
+          break;
+        }
+        if (warp == 0 && lane == 0) sy.flags[2] = q + 1;
+        ++q;
+        if (2 * group < strips) {
+          const int n = min(step, kb - b);
+          // this warp's blocks: those whose place along K is `slice` modulo the slices
+          const int f = (slice - b) & (slices - 1);
+          const uint32_t st = smem_u32(w4sm) + pos.s * STAGE;
+          // a unit's odd last strip is multiplied twice; the second sum is not read
+          const uint32_t to1 = 2 * group + 1 < strips ? n * R : 0;
+          uint32_t xr[NB];
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            xr[j] = st + strips * n * R + min(g + 8 * j, rows - 1) * (128 * n + 64) + 128 * f + 16 * t;
+          w4s_blocks<NB, G32, ZP>(acc, (n - f + slices - 1) >> (3 - lg),
+                                  st + (2 * group * n + f) * R + 16 * lane, to1, slices * R, xr, 128 * slices,
+                                  64, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.empty(pos.s));
+        pos.next();
+      }
+      if (!ok) break;
+      // hand the unit's partial sums (or the end) to the joining warps
+      const int buf = n_unit & 1;
+      if (n_unit >= 2 && !w4s_wait(sy.acc_empty(buf), ((n_unit >> 1) - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      if (warp == 0 && lane == 0) acc_unit[buf] = make_int4(unit, strips, rows, lg);
+      if (unit >= 0)
+        w4s_put<NB>(acc, smem_u32(acc_tiles) + buf * w4s_acc_bytes<NB>(), ((slice << lg) + group) * 2, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sy.acc_full(buf));
+      if (unit < 0) break;
+    }
+    if (!ok) sy.abort();
   } else {
     const int et = tid - 32 * W4S_MMA_WARPS;
     for (int n = 0;; ++n) {
-      const int b = n & 1;
-      if (!w4s_wait(bar.acc_full(b), (n >> 1) & 1)) {
-        *reinterpret_cast<volatile int*>(L.abort_flag) = 1;
+      const int buf = n & 1;
+      if (sy.aborted() || !w4s_wait(sy.acc_full(buf), (n >> 1) & 1)) {
+        sy.abort();
         break;
       }
-      const int4 u = L.acc_unit[b];
+      const int4 u = acc_unit[buf];
       if (u.x < 0) break;
-      const float* acc = L.acc + b * (w4s_acc_bytes<NB>() / 4);
-      const bool down = u.x >= U1;
-      const int v = down ? u.x - U1 : u.x, per = down ? nb2 : strips1, ai = v / per, blk = v - ai * per;
+      const float* acc = acc_tiles + buf * (w4s_acc_bytes<NB>() / 4);
+      bool down;
+      int ai, blk;
+      split(u.x, down, ai, blk);
       const int off = list.off[ai];
       if (!down) {
-        for (int i = et; i < 16 * u.z; i += 32 * W4S_EPI_WARPS) {
+        for (int i = et; i < 16 * u.z; i += W4S_EPI_THREADS) {
           const int r = i & 15, c = i >> 4;
           const float gt = w4s_join<NB>(acc, 0, 0, c, r), up = w4s_join<NB>(acc, 0, 1, c, r);
           a.h[(size_t)list.pair[off + c] * a.I + 16 * blk + r] = __float2bfloat16_rn(w4_geglu(gt, up));
@@ -437,21 +621,21 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
         const int n0 = (blk << (a.lg2 + 1)) * W4_ROWS;
         for (int c = 0; c < u.z; ++c) {
           float* o = a.o + (size_t)list.pair[off + c] * a.H + n0;
-          const float w = list.w[off + c];
-          for (int i = et; i < 16 * u.y; i += 32 * W4S_EPI_WARPS)
-            o[i] = w * w4s_join<NB>(acc, u.w, i >> 4, c, i & 15);
+          for (int i = et; i < 16 * u.y; i += W4S_EPI_THREADS)
+            o[i] = w4s_join<NB>(acc, u.w, i >> 4, c, i & 15);
         }
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar.acc_empty(b));
+        mbar_arrive(sy.acc_empty(buf));
         red_release_add_gpu(down ? o_ready + blk : h_ready + ai, 1);
+        if (!down) red_release_add_gpu(a.ctr + 4, 1);
       }
     }
   }
   __syncthreads();
-  if (*reinterpret_cast<volatile int*>(L.abort_flag)) {
-    if (tid == 0) w4s_drain<NB>(L);
+  if (sy.aborted()) {
+    if (tid == 0) sy.drain();
     return;
   }
   // ---- the weighted sum of each token's slots, in slot order: this CTA's share of four outputs
@@ -460,14 +644,16 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
   const int share = (items + gridDim.x - 1) / gridDim.x;
   for (int i = blockIdx.x * share + tid; i < min(items, (int)(blockIdx.x + 1) * share); i += W4S_THREADS) {
     const int t = i / quads, n = 4 * (i - t * quads);
-    if (!wait_counter_geq(o_ready + (n / W4_ROWS >> (a.lg2 + 1)), W4S_EPI_WARPS * n_act)) return;
+    if (!w4m_wait(o_ready + (n / W4_ROWS >> (a.lg2 + 1)), W4S_EPI_WARPS * n_act) || !w4m_wait(a.ctr + 3, a.T))
+      return;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < a.k; ++j) {
       const float4 p = __ldcg(reinterpret_cast<const float4*>(a.o + ((size_t)t * a.k + j) * a.H + n));
-      v.x += p.x;
-      v.y += p.y;
-      v.z += p.z;
-      v.w += p.w;
+      const float w = __ldcg(a.wts + (size_t)t * a.k + j);
+      v.x = fmaf(w, p.x, v.x);
+      v.y = fmaf(w, p.y, v.y);
+      v.z = fmaf(w, p.z, v.z);
+      v.w = fmaf(w, p.w, v.w);
     }
     uint2 r;
     r.x = pack_bf16x2(v.x, v.y);

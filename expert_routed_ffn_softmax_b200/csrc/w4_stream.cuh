@@ -1,21 +1,25 @@
 // w4_stream.cuh -- products of a few activation rows (at most 16) with packed 4-bit weights, as
-// one stream of weight bytes: the linear layer, the two halves of the dense GEGLU MLP, and the
-// routed experts of a whole MoE layer (w4_moe.cuh) are the same pipeline over different units.
+// one stream of weight bytes: the linear layer and the two halves of the dense GEGLU MLP here, the
+// routed experts of a whole MoE layer in w4_moe.cuh.
 //
 // What bounds it.  At T <= 16 a weight byte meets at most 64 flops, so the work is reading the
-// weights once at the memory's rate, decoding two weights per byte on the way.  Per SM that is
-// about 23 bytes (46 weights) a clock, 45 % of the issue slots for the decode at T <= 8.
+// weights once at the memory's rate, decoding two weights per byte on the way: per SM about 23
+// bytes (46 weights) a clock.  The decode and the products of a block (1024 weights) take 23 to 25
+// clocks of an SM (measured by repeating them), its bytes 22 to 24: both must run at once.
 //
-// Roles of a CTA (13 warps, two CTAs per SM so that one decodes while the other joins or waits):
-//   warp 12      producer: copies each unit in chunks of consecutive blocks with bulk copies --
-//                one per strip (codes and scales of a strip's run of blocks are contiguous) and
-//                one per activation row -- into a ring of stages, up to 90 KB ahead;
-//   warps 0-7    multiply: warp = (row group of two strips) x (slice of the blocks along K); a
-//                block is one 16-byte shared read per lane, decoded in registers into operands
-//                of the matrix instruction (w4_block);
-//   warps 8-11   join the K slices' fp32 sums through a double-buffered accumulator tile in
-//                shared memory, in a fixed order, and write the outputs, while the multiply
-//                warps are at the next unit.
+// Roles of a CTA (two CTAs per SM, so that one multiplies while the other joins or waits):
+//   producer     one thread copies each unit in chunks of consecutive blocks, one bulk copy per
+//                strip (a strip's run of blocks is contiguous), into a ring of stages.  Its code
+//                per chunk is kept to the copies: beside warps that issue all the time every
+//                instruction of it costs some ten clocks (with a header and a table per chunk and
+//                the activations copied along it took 2000 to 3600 clocks a chunk and the stream
+//                ran at 0.3 to 0.6 of the memory's rate);
+//   multiply     8 warps = row groups of two strips x slices of the blocks along K; a block is one
+//                16-byte shared read per lane, decoded in registers into operands of the matrix
+//                instruction (w4_block);
+//   join         2 warps add the K slices' fp32 sums through an accumulator tile in shared memory,
+//                in a fixed order, and write the outputs, while the multiply warps are at the next
+//                unit.
 // Every wait is bounded; a wait that runs out sets the device error word and ends the CTA after
 // its copies in flight have landed.
 #pragma once
@@ -24,99 +28,19 @@
 
 namespace moe {
 
-constexpr int W4S_MMA_WARPS = 8, W4S_EPI_WARPS = 4;
+constexpr int W4S_MMA_WARPS = 8, W4S_EPI_WARPS = 2;
 constexpr int W4S_THREADS = 32 * (W4S_MMA_WARPS + W4S_EPI_WARPS + 1);
-constexpr int W4S_COL = 20;    // floats per accumulator column (16 rows, padded against conflicts)
-// Ring stages and their bytes: two CTAs per SM, activation tiles of 8 (NB = 1) or 16 rows.
-template <int NB> struct W4Ring;
-template <> struct W4Ring<1> { static constexpr int STAGES = 3, BYTES = 30720; };
-template <> struct W4Ring<2> { static constexpr int STAGES = 3, BYTES = 23552; };
+constexpr int W4S_EPI_THREADS = 32 * W4S_EPI_WARPS;
+constexpr int W4S_STAGES = 3;
+constexpr int W4S_COL = 20;             // floats per accumulator column (16 rows, padded)
+constexpr int W4S_SMEM = 115712;        // two CTAs per SM
+// accumulator tile: 16 (K slice, strip) pairs x 8 NB columns
 template <int NB> __host__ __device__ constexpr int w4s_acc_bytes() { return 16 * 8 * NB * W4S_COL * 4; }
-constexpr int W4S_MISC = 3072;
-template <int NB> __host__ __device__ constexpr int w4s_smem() {
-  return W4Ring<NB>::STAGES * W4Ring<NB>::BYTES + 2 * w4s_acc_bytes<NB>() + W4S_MISC;
-}
 
-enum W4Mode { W4_LINEAR = 0, W4_LINEAR_F32 = 1, W4_GEGLU = 2, W4_MOE = 3 };
-
-// What a stage holds, written by the producer before the stage's barrier completes: the common
-// part, and where each multiply warp finds its share (so that it computes next to nothing).
-struct __align__(16) W4Chunk {
-  int unit;       // -1: no more work
-  int last;       // 1: the unit's last chunk
-  int strips;     // strips of the unit
-  int lg;         // log2 of the row groups (of two strips) that the multiply warps are split over
-  int rows;       // activation rows
-  int x_pitch;    // bytes between them
-  int slices;     // slices along K: a warp takes every slices-th block
-  int pad;
-  struct __align__(16) Share {
-    uint32_t w;   // first block's record of the first strip
-    uint32_t to1; // bytes to the same record of the second strip
-    uint32_t x;   // row 0's activations of the first block
-    int n;        // blocks
-  } share[W4S_MMA_WARPS];
-};
-
-struct W4Smem {
-  uint32_t bars;          // full[S], empty[S], acc_full[2], acc_empty[2]
-  W4Chunk* chunk;         // [S]
-  int4* acc_unit;         // [2] {unit, strips, rows, log2 row groups}
-  int* abort_flag;
-  int* issued;            // chunks issued / consumed, for the drain after a failure
-  int* consumed;
-  float* acc;             // [2][16][8 NB][W4S_COL]
-  int* list;              // the rest of the miscellaneous bytes (routed layer)
-};
-template <int NB>
-__device__ __forceinline__ W4Smem w4s_layout(uint8_t* sm) {
-  constexpr int S = W4Ring<NB>::STAGES;
-  uint8_t* p = sm + S * W4Ring<NB>::BYTES;
-  W4Smem L;
-  L.acc = reinterpret_cast<float*>(p);
-  p += 2 * w4s_acc_bytes<NB>();
-  L.bars = smem_u32(p);
-  p += (8 * (2 * S + 4) + 15) / 16 * 16;
-  L.chunk = reinterpret_cast<W4Chunk*>(p);
-  p += sizeof(W4Chunk) * S;
-  L.acc_unit = reinterpret_cast<int4*>(p);
-  p += 32;
-  L.abort_flag = reinterpret_cast<int*>(p);
-  L.issued = L.abort_flag + 1;
-  L.consumed = L.abort_flag + 2;
-  L.list = L.abort_flag + 4;
-  return L;
-}
-template <int NB>
-struct W4Bars {
-  static constexpr int S = W4Ring<NB>::STAGES;
-  uint32_t base;
-  __device__ uint32_t full(int s) const { return base + 8u * s; }
-  __device__ uint32_t empty(int s) const { return base + 8u * (S + s); }
-  __device__ uint32_t acc_full(int b) const { return base + 8u * (2 * S + b); }
-  __device__ uint32_t acc_empty(int b) const { return base + 8u * (2 * S + 2 + b); }
-};
-
-template <int NB>
-__device__ __forceinline__ void w4s_init(const W4Smem& L) {
-  const W4Bars<NB> bar{L.bars};
-  for (int s = 0; s < W4Ring<NB>::STAGES; ++s) {
-    mbar_init(bar.full(s), 1);
-    mbar_init(bar.empty(s), W4S_MMA_WARPS);
-  }
-  for (int b = 0; b < 2; ++b) {
-    mbar_init(bar.acc_full(b), W4S_MMA_WARPS);
-    mbar_init(bar.acc_empty(b), W4S_EPI_WARPS);
-  }
-  *L.abort_flag = 0;
-  *L.issued = 0;
-  *L.consumed = 0;
-  fence_barrier_init();
-}
+enum W4Mode { W4_LINEAR = 0, W4_LINEAR_F32 = 1, W4_GEGLU = 2 };
 
 // Bounded wait for warps that wait long and often beside warps that compute: the hint lets the
-// hardware park the warp until the phase completes.  Without it a try_wait returns after some 150
-// clocks and the waiting warps' loops took 37 % of the SM's instructions (ncu, T = 1).
+// hardware park the warp until the phase completes.
 __device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity) {
   constexpr uint32_t kParkNs = 20000;
   uint64_t t0 = 0;
@@ -139,170 +63,99 @@ __device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
-// Blocks per chunk: as many as fit a stage, evened out over the unit.  Activation rows keep 64
-// bytes between them, so that two rows' 64-byte fragments fall in different halves of the banks.
-template <int NB, int R>
-__device__ __forceinline__ int w4s_chunk_blocks(int kb, int strips, int rows) {
-  const int most = (W4Ring<NB>::BYTES - 64 * rows) / (strips * R + 128 * rows);
-  const int chunks = (kb + most - 1) / most;
-  return (kb + chunks - 1) / chunks;
-}
-
-// A unit for the producer: strips' bytes, activation rows.
-struct W4Unit {
-  const uint8_t *s0, *s1;     // strips 0 and 1 (further strips follow s0 at `pitch`)
-  size_t pitch;
-  int id, strips, rows, lg, kb;
-};
-
-// The producer's side of the ring.
-template <int NB, int R>
-struct W4Producer {
-  const W4Smem& L;
-  uint8_t* ring;
-  int lane, q = 0;
-
-  // Wait for the next stage, announce the chunk and start its weight copies.  All lanes call.
-  __device__ bool weights(const W4Unit& u, int first, int blocks, int qq) {
-    constexpr int S = W4Ring<NB>::STAGES;
-    const W4Bars<NB> bar{L.bars};
-    const int s = qq % S;
-    if (*reinterpret_cast<volatile int*>(L.abort_flag) ||
-        (qq >= S && !w4s_wait(bar.empty(s), ((qq / S) - 1) & 1)))
-      return false;
-    const uint32_t at = smem_u32(ring + s * W4Ring<NB>::BYTES);
-    if (lane < W4S_MMA_WARPS) {
-      // share of multiply warp `lane`: blocks whose index along K is its slice modulo the slices
-      const int slices = W4S_MMA_WARPS >> u.lg, group = lane & ((1 << u.lg) - 1), slice = lane >> u.lg;
-      const int b = (slice - first) & (slices - 1);
-      W4Chunk::Share sh;
-      sh.w = at + (2 * group * blocks + b) * R;
-      // a unit's odd last strip is multiplied twice; the second sum is not read
-      sh.to1 = 2 * group + 1 < u.strips ? blocks * R : 0;
-      sh.x = at + u.strips * blocks * R + 128 * b;
-      sh.n = 2 * group < u.strips ? (blocks - b + slices - 1) >> (3 - u.lg) : 0;
-      L.chunk[s].share[lane] = sh;
-      if (lane == 0) {
-        int4* c = reinterpret_cast<int4*>(&L.chunk[s]);
-        c[0] = make_int4(u.id, first + blocks >= u.kb, u.strips, u.lg);
-        c[1] = make_int4(u.rows, 128 * blocks + 64, slices, 0);
-        *reinterpret_cast<volatile int*>(L.issued) = qq + 1;
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(bar.full(s), (uint32_t)(blocks * (u.strips * R + 128 * u.rows)));
-    __syncwarp();
-    if (lane < u.strips) {
-      const uint8_t* src = (lane == 1 ? u.s1 : u.s0 + lane * u.pitch) + (size_t)first * R;
-      bulk_load(at + lane * blocks * R, src, blocks * R, bar.full(s));
-    }
-    return true;
+// Barriers and flags of a CTA.
+struct W4Sync {
+  uint32_t base;
+  volatile int* flags;   // {abort, chunks issued, chunks consumed, activations issued}
+  __device__ uint32_t full(int s) const { return base + 8u * s; }
+  __device__ uint32_t empty(int s) const { return base + 8u * (W4S_STAGES + s); }
+  __device__ uint32_t acc_full(int b) const { return base + 8u * (2 * W4S_STAGES + b); }
+  __device__ uint32_t acc_empty(int b) const { return base + 8u * (2 * W4S_STAGES + 2 + b); }
+  __device__ uint32_t act_full() const { return base + 8u * (2 * W4S_STAGES + 4); }
+  __device__ uint32_t steal_full() const { return base + 8u * (2 * W4S_STAGES + 5); }
+  static constexpr int BYTES = 8 * (2 * W4S_STAGES + 6) + 16;   // 112
+  __device__ void init(uint8_t* at) {
+    base = smem_u32(at);
+    flags = reinterpret_cast<volatile int*>(at + 8 * (2 * W4S_STAGES + 6));
   }
-  // Start the chunk's activation copies (row: this lane's row, for lanes < u.rows).
-  __device__ void rows(const W4Unit& u, int first, int blocks, int qq, const __nv_bfloat16* row) {
-    constexpr int S = W4Ring<NB>::STAGES;
-    const W4Bars<NB> bar{L.bars};
-    const int s = qq % S;
-    if (lane < u.rows)
-      bulk_load(smem_u32(ring + s * W4Ring<NB>::BYTES) + u.strips * blocks * R +
-                    lane * (128 * blocks + 64),
-                row + 64 * first, 128 * blocks, bar.full(s));
-  }
-  __device__ bool stop() {
-    constexpr int S = W4Ring<NB>::STAGES;
-    const W4Bars<NB> bar{L.bars};
-    const int s = q % S;
-    if (q >= S && !w4s_wait(bar.empty(s), ((q / S) - 1) & 1)) return false;
-    if (lane == 0) {
-      L.chunk[s].unit = -1;
-      mbar_arrive(bar.full(s));
+  __device__ void reset() const {
+    for (int s = 0; s < W4S_STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), W4S_MMA_WARPS);
     }
-    return true;
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), W4S_MMA_WARPS);
+      mbar_init(acc_empty(b), W4S_EPI_WARPS);
+    }
+    mbar_init(act_full(), 1);
+    mbar_init(steal_full(), 1);
+    flags[0] = flags[1] = flags[2] = flags[3] = 0;
+    fence_barrier_init();
+  }
+  __device__ void abort() const { flags[0] = 1; }
+  __device__ bool aborted() const { return flags[0] != 0; }
+  // After the roles have ended with an abort: wait for chunks that were issued and not consumed.
+  __device__ void drain() const {
+    for (int q = flags[2]; q < flags[1]; ++q)
+      mbar_wait_ns(full(q % W4S_STAGES), (q / W4S_STAGES) & 1, kDrainLimitNs);
+    if (flags[3]) mbar_wait_ns(act_full(), 0, kDrainLimitNs);
   }
 };
 
-// Multiply warps.
-template <int NB, bool G32, bool ZP>
-__device__ __forceinline__ void w4s_multiply(const W4Smem& L, int warp, int lane) {
-  constexpr int S = W4Ring<NB>::STAGES;
-  constexpr int R = 512 + (G32 ? 2 : 1) * (ZP ? 48 : 32);
-  const W4Bars<NB> bar{L.bars};
-  const int g = lane >> 2, t = lane & 3;
-  const uint32_t chunk_at = smem_u32(L.chunk), acc_at = smem_u32(L.acc);
-  float acc[2][NB][4];
-#pragma unroll
-  for (int i = 0; i < 2 * NB * 4; ++i) acc[i / (4 * NB)][i / 4 % NB][i % 4] = 0.f;
-  int n_acc = 0, s = 0;
+// Position in the ring: stage and the parity of its current phase.
+struct W4Pos {
+  int s = 0;
   uint32_t phase = 0;
-  for (int q = 0;; ++q) {
-    if (!w4s_wait(bar.full(s), phase)) {
-      *reinterpret_cast<volatile int*>(L.abort_flag) = 1;
-      return;
-    }
-    const uint32_t head = chunk_at + s * (uint32_t)sizeof(W4Chunk);
-    const uint4 h0 = lds_v4<0>(head), h1 = lds_v4<16>(head);
-    const int unit = (int)h0.x, last = h0.y, strips = h0.z, lg = h0.w, rows = h1.x;
-    if (warp == 0 && lane == 0) *reinterpret_cast<volatile int*>(L.consumed) = q + 1;
-    if (unit >= 0) {
-      const uint4 share = lds_v4<32>(head + 16 * warp);
-      uint32_t w = share.x + 16 * lane, xr[NB];
-      const uint32_t w_step = h1.z * R, x_step = h1.z * 128;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) xr[j] = share.z + min(g + 8 * j, rows - 1) * h1.y + 16 * t;
-#pragma unroll 1
-      for (int n = share.w; n > 0; --n) {
-        const uint32_t rec[2] = {w, w + share.y};
-        w4_block<2, NB, G32, ZP>(acc, rec, lane, xr);
-        w += w_step;
-#pragma unroll
-        for (int j = 0; j < NB; ++j) xr[j] += x_step;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.empty(s));
-    }
-    if (++s == S) {
+  __device__ void next() {
+    if (++s == W4S_STAGES) {
       s = 0;
       phase ^= 1;
     }
-    if (unit >= 0 && !last) continue;
-    // hand the unit's partial sums (or the end) to the joining warps
-    const int b = n_acc & 1;
-    if (n_acc >= 2 && !w4s_wait(bar.acc_empty(b), ((n_acc >> 1) - 1) & 1)) {
-      *reinterpret_cast<volatile int*>(L.abort_flag) = 1;
-      return;
-    }
-    if (warp == 0 && lane == 0) L.acc_unit[b] = make_int4(unit, strips, rows, lg);
-    if (unit >= 0) {
-      const int group = warp & ((1 << lg) - 1), slice = warp >> lg;
-      const uint32_t dst = acc_at + b * w4s_acc_bytes<NB>() +
-                           4 * ((((slice << lg) + group) * 16 * NB + 2 * t) * W4S_COL + g);
+  }
+};
+
+// acc += this warp's blocks of one chunk: n blocks from record address w (+ 16 lane, strip 0; strip
+// 1 at + to1) every w_step bytes, activations at xr every x_step bytes (a block's second half at
+// + x_half).
+template <int NB, bool G32, bool ZP>
+__device__ __forceinline__ void w4s_blocks(float (&acc)[2][NB][4], int n, uint32_t w, uint32_t to1,
+                                           uint32_t w_step, uint32_t (&xr)[NB], uint32_t x_step,
+                                           uint32_t x_half, int lane) {
+#pragma unroll 1
+  for (; n > 0; --n) {
+    const uint32_t rec[2] = {w, w + to1};
+    w4_block<2, NB, G32, ZP>(acc, rec, lane, xr, x_half);
+    w += w_step;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(
-                             dst + 4 * (((i * NB + j) * 8 + (v & 1)) * W4S_COL + 8 * (v >> 1))),
-                         "f"(acc[i][j][v])
-                         : "memory");
-            acc[i][j][v] = 0.f;
-          }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar.acc_full(b));
-    if (unit < 0) return;
-    ++n_acc;
+    for (int j = 0; j < NB; ++j) xr[j] += x_step;
   }
 }
 
+// Store this warp's partial sums into the accumulator tile at `tile` (entry = K slice x strips +
+// strip) and clear them.
+template <int NB>
+__device__ __forceinline__ void w4s_put(float (&acc)[2][NB][4], uint32_t tile, int entry, int lane) {
+  const uint32_t dst = tile + 4 * ((entry * 8 * NB + 2 * (lane & 3)) * W4S_COL + (lane >> 2));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                         dst + 4 * (((i * NB + j) * 8 + (v & 1)) * W4S_COL + 8 * (v >> 1))),
+                     "f"(acc[i][j][v])
+                     : "memory");
+        acc[i][j][v] = 0.f;
+      }
+}
 // Sum over the K slices, in slice order, of one accumulator element.
 template <int NB>
 __device__ __forceinline__ float w4s_join(const float* acc, int lg, int strip, int col, int row) {
   const float* p = acc + (strip * 8 * NB + col) * W4S_COL + row;
   float v = 0.f;
   for (int s = 0; s < W4S_MMA_WARPS >> lg; ++s) v += p[(s * 2 * 8 * NB * W4S_COL) << lg];
-  return v;
+  return 4.f * v;   // the decoded weights are quarters
 }
 
 // gelu_tanh(a) * u.  tanh.approx.f32 (documented: relative error 2^-11) is far below the
@@ -312,125 +165,300 @@ __device__ __forceinline__ float w4_geglu(float a, float u) {
   return 0.5f * a * (1.f + th) * u;
 }
 
-// After the roles have ended: wait for copies that were issued and not consumed.
+// ----------------------------------------------------------------------------- work stealing
+// Take over a CTA of this grid that has not started (cluster launch control): the answer, 16 bytes
+// at `answer`, completes on `bar`.  SMs stream at different rates, so units dealt out in advance
+// end at the pace of the slowest SM; this hands them out as CTAs become free, without a counter
+// that something would have to zero before each launch.
+__device__ __forceinline__ void steal_request(uint32_t answer, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          answer),
+      "r"(bar)
+      : "memory");
+}
+// The taken CTA's blockIdx.x, or -1 when none was left (no further request may follow then).
+__device__ __forceinline__ int steal_answer(uint32_t answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  fence_proxy_async_smem();   // this read before the next answer is written
+  return got ? (int)x : -1;
+}
+
+// ----------------------------------------------------------------------------- activations
+// Activations in the multiply warps' order ("fragments"): per block along K 2 halves x NB row tiles
+// x 32 lanes x 16 bytes, lane 4 g + t of (h, j) holding elements 64 b + 32 h + 8 t .. + 7 of row
+// g + 8 j.  Rows past T hold anything: they only reach outputs that are not stored.
 template <int NB>
-__device__ __forceinline__ void w4s_drain(const W4Smem& L) {
-  const W4Bars<NB> bar{L.bars};
-  const int to = *reinterpret_cast<volatile int*>(L.issued);
-  for (int q = *reinterpret_cast<volatile int*>(L.consumed); q < to; ++q)
-    mbar_wait_ns(bar.full(q % W4Ring<NB>::STAGES), (q / W4Ring<NB>::STAGES) & 1, kDrainLimitNs);
+__host__ __device__ constexpr int w4_frag_block() { return 2 * NB * 512; }
+__host__ __device__ inline size_t w4_frag_index(int nb, int row, int k) {   // in elements
+  return ((((size_t)(k >> 6) * 2 + ((k >> 5) & 1)) * nb + (row >> 3)) * 32 + 4 * (row & 7) + ((k >> 3) & 3)) * 8 +
+         (k & 7);
+}
+// x [T][K] -> fragments, one 16-byte vector a thread.
+__global__ void __launch_bounds__(256) w4_fragment_kernel(const __nv_bfloat16* __restrict__ x, int T, int K,
+                                                          int nb, __nv_bfloat16* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const int per = K / 8;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < T * per; i += gridDim.x * 256) {
+    const int row = i / per, k = 8 * (i - row * per);
+    *reinterpret_cast<uint4*>(out + w4_frag_index(nb, row, k)) =
+        __ldg(reinterpret_cast<const uint4*>(x + (size_t)row * K + k));
+  }
 }
 
 // ----------------------------------------------------------------------------- linear, GEGLU
 struct W4Linear {
   const uint8_t *w0, *w1;       // packed matrix; gate and up for GEGLU
-  const __nv_bfloat16* act;     // [T][K]
+  const __nv_bfloat16* act;     // [T][K], or fragments
   void* out;                    // [T][N]
-  int T, K, N, lg, units;
+  int T, K, N;
+  int lg;                       // log2 of the row groups: 2 << lg strips per unit
+  int units, step;              // blocks per chunk
+  int stage;                    // bytes of a stage
+  int frag;                     // 1: act holds fragments and a chunk brings its blocks' along;
+                                // 0: a CTA keeps all of act in shared memory
+  int out_frag;                 // GEGLU: h is written as fragments of this many row tiles (or 0)
+  int steal;                    // 1: more units than CTAs run at once
   int early;                    // 1: the previous kernel does not write the weights and started
-                                // after every kernel before it had ended (dense MLP): the first
-                                // weight copies may start before it has ended
+                                // after every kernel before it had ended: the first weight
+                                // copies may start before it has ended
 };
 
-// Units: 2 << lg strips (GEGLU: the gate and up strips of 16 features), dealt round robin.
+// Shared memory: ring, activations (rows 64 bytes apart, so that the two rows a quarter warp reads
+// fall in different halves of the banks), accumulator tiles, ids, barriers.
+struct W4LinearSmem {
+  int act, acc, answer, unit, sync, total;
+};
+constexpr int W4S_UNITS = W4S_STAGES + 1;   // unit ids in flight from the producer to the others
+template <int NB>
+__host__ __device__ inline W4LinearSmem w4_linear_smem(int T, int K, int frag, int stage) {
+  W4LinearSmem L;
+  L.act = W4S_STAGES * stage;
+  L.acc = L.act + (frag ? 0 : T * (2 * K + 64));
+  L.answer = L.acc + 2 * w4s_acc_bytes<NB>();
+  L.unit = L.answer + 16;
+  L.sync = L.unit + 4 * (W4S_UNITS + 2 + 2);
+  L.total = L.sync + W4Sync::BYTES;
+  return L;
+}
+
+// Units: 2 << lg strips (GEGLU: the gate and up strips of 16 << lg features, in turn).  A CTA
+// starts with the unit of its block index and takes over units of CTAs that have not started.
 template <int NB, bool G32, bool ZP, int MODE>
-__global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(W4Linear a) {
+__global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_constant__ W4Linear a) {
   constexpr int R = 512 + (G32 ? 2 : 1) * (ZP ? 48 : 32);
+  constexpr int FB = w4_frag_block<NB>();
   extern __shared__ __align__(128) uint8_t w4sm[];
-  const W4Smem L = w4s_layout<NB>(w4sm);
-  const W4Bars<NB> bar{L.bars};
+  const W4LinearSmem SL = w4_linear_smem<NB>(a.T, a.K, a.frag, a.stage);
+  W4Sync sy;
+  sy.init(w4sm + SL.sync);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) w4s_init<NB>(L);
-  __syncthreads();
+  if (tid == 0) sy.reset();
   if (!a.early) {
     pdl_wait();
     pdl_trigger();
   }
-  const int kb = a.K / W4_KB;
+  // nothing is done when an earlier launch's wait has run out
+  if (tid == 0 && (*reinterpret_cast<volatile unsigned*>(&g_error_word) & MOE_DEVERR_TIMEOUT)) sy.abort();
+  __syncthreads();
+  // unit ids: from the producer to the multiply warps (rewritten only after every multiply warp
+  // has released a later unit's chunk), and on to the joining warps
+  int* unit_ring = reinterpret_cast<int*>(w4sm + SL.unit);
+  int* acc_unit = unit_ring + W4S_UNITS;
+  const int blocks = a.K / W4_KB, strips_all = a.N / W4_ROWS;
+  // strips of unit u (its matrix, or of each of gate and up)
+  auto strips_of = [&](int u) {
+    return MODE == W4_GEGLU ? min(1 << a.lg, strips_all - (u << a.lg))
+                            : min(2 << a.lg, strips_all - (u << (a.lg + 1)));
+  };
   if (warp == W4S_MMA_WARPS + W4S_EPI_WARPS) {
-    W4Producer<NB, R> p{L, w4sm, lane};
-    // no units when an earlier launch's wait has run out
-    int units = 0;
-    if (lane == 0 && !(*reinterpret_cast<volatile unsigned*>(&g_error_word) & MOE_DEVERR_TIMEOUT))
-      units = a.units;
-    units = __shfl_sync(0xffffffffu, units, 0);
-    const __nv_bfloat16* row = a.act + (size_t)min(lane, a.T - 1) * a.K;
-    bool ok = true, waited = !a.early;
-    fence_proxy_async_global();
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      W4Unit un;
-      const int s0 = MODE == W4_GEGLU ? u : u << (a.lg + 1);
-      un.pitch = (size_t)kb * R;
-      un.s0 = a.w0 + s0 * un.pitch;
-      un.s1 = MODE == W4_GEGLU ? a.w1 + s0 * un.pitch : un.s0 + un.pitch;
-      un.id = u;
-      un.strips = MODE == W4_GEGLU ? 2 : min(2 << a.lg, a.N / W4_ROWS - s0);
-      un.rows = a.T;
-      un.lg = a.lg;
-      un.kb = kb;
-      const int step = w4s_chunk_blocks<NB, R>(kb, un.strips, un.rows);
-      int first = 0;
-      if (!waited) {
-        // the first stages' weights before the previous kernel has ended, then its rows
-        const int pre = min((kb + step - 1) / step, W4Ring<NB>::STAGES);
-        for (int i = 0; i < pre && ok; ++i)
-          ok = p.weights(un, i * step, min(step, kb - i * step), p.q + i);
+    if (lane == 0) {
+      const uint32_t ring = smem_u32(w4sm), answer = smem_u32(w4sm + SL.answer);
+      const size_t pitch = (size_t)blocks * R;
+      bool ok = !sy.aborted(), waited = !a.early;
+      int q = 0, n_unit = 0, n_steal = 0;
+      W4Pos pos;
+      // act, once the previous kernel has ended: all of it, or the fragments of the chunks whose
+      // weights are on their way already
+      auto activations = [&](int chunks) {
+        fence_proxy_async_global();
+        if (!a.frag) {
+          sy.flags[3] = 1;
+          mbar_arrive_expect_tx(sy.act_full(), a.T * 2 * a.K);
+          for (int t = 0; t < a.T; ++t)
+            bulk_load(smem_u32(w4sm + SL.act) + t * (2 * a.K + 64), a.act + (size_t)t * a.K, 2 * a.K, sy.act_full());
+        }
+        for (int i = 0; a.frag && i < chunks; ++i) {
+          const int n = min(a.step, blocks - i * a.step), ns = (MODE == W4_GEGLU ? 2 : 1) * strips_of(blockIdx.x);
+          bulk_load(ring + i * a.stage + ns * n * R, a.act + (size_t)i * a.step * (FB / 2), n * FB, sy.full(i));
+        }
+        waited = true;
+      };
+      auto wait_previous = [&](int chunks) {
         pdl_wait();
         pdl_trigger();
-        fence_proxy_async_global();
-        waited = true;
-        for (int i = 0; i < pre && ok; ++i)
-          p.rows(un, i * step, min(step, kb - i * step), p.q + i, row);
-        p.q += pre;
-        first = pre * step;
+        activations(chunks);
+      };
+      if (ok && waited) activations(0);
+      for (int u = blockIdx.x; u >= 0 && ok; ++n_unit) {
+        unit_ring[n_unit % W4S_UNITS] = u;
+        if (a.steal) steal_request(answer, sy.steal_full());
+        const int ns = strips_of(u), all = MODE == W4_GEGLU ? 2 * ns : ns;
+        const size_t at = ((size_t)u << (MODE == W4_GEGLU ? a.lg : a.lg + 1)) * pitch;
+        for (int b = 0; b < blocks; b += a.step, ++q, pos.next()) {
+          // in the first unit weights go ahead until the ring is full
+          if (!waited && q == W4S_STAGES) wait_previous(q);
+          if (sy.aborted() || (q >= W4S_STAGES && !w4s_wait(sy.empty(pos.s), pos.phase ^ 1))) {
+            ok = false;
+            break;
+          }
+          const int n = min(a.step, blocks - b);
+          const uint32_t bytes = n * R, bar = sy.full(pos.s);
+          uint32_t dst = ring + pos.s * a.stage;
+          const uint8_t* src = a.w0 + at + (size_t)b * R;
+          sy.flags[1] = q + 1;
+          mbar_arrive_expect_tx(bar, all * bytes + (a.frag ? n * FB : 0));
+          if (MODE == W4_GEGLU) {
+            const uint8_t* up = a.w1 + at + (size_t)b * R;
+            for (int i = 0; i < ns; ++i, src += pitch, up += pitch, dst += 2 * bytes) {
+              bulk_load(dst, src, bytes, bar);
+              bulk_load(dst + bytes, up, bytes, bar);
+            }
+          } else {
+            for (int i = 0; i < ns; ++i, src += pitch, dst += bytes) bulk_load(dst, src, bytes, bar);
+          }
+          if (a.frag && waited) bulk_load(dst, a.act + (size_t)b * (FB / 2), n * FB, bar);
+        }
+        if (!waited) wait_previous(q);
+        u = -1;
+        if (a.steal) {
+          // also when giving up: the answer must not arrive in a CTA that has ended
+          if (!w4s_wait(sy.steal_full(), n_steal & 1)) ok = false;
+          else u = steal_answer(answer);
+          ++n_steal;
+        }
       }
-      for (; first < kb && ok; first += step) {
-        const int n = min(step, kb - first);
-        ok = p.weights(un, first, n, p.q);
-        if (ok) p.rows(un, first, n, p.q, row);
-        ++p.q;
+      if (!waited) pdl_wait();
+      if (ok) {
+        // the end, through a stage of its own
+        if (q >= W4S_STAGES && !w4s_wait(sy.empty(pos.s), pos.phase ^ 1)) ok = false;
+        unit_ring[n_unit % W4S_UNITS] = -1;
+        if (ok) mbar_arrive(sy.full(pos.s));
       }
+      if (!ok) sy.abort();
     }
-    if (!waited) pdl_wait();
-    if (ok) ok = p.stop();
-    if (!ok) *reinterpret_cast<volatile int*>(L.abort_flag) = 1;
   } else if (warp < W4S_MMA_WARPS) {
-    w4s_multiply<NB, G32, ZP>(L, warp, lane);
-  } else {
-    const int et = tid - 32 * W4S_MMA_WARPS;
-    if (a.early) pdl_wait();   // outputs may be what the previous kernel still reads
-    for (int n = 0;; ++n) {
-      const int b = n & 1;
-      if (!w4s_wait(bar.acc_full(b), (n >> 1) & 1)) {
-        *reinterpret_cast<volatile int*>(L.abort_flag) = 1;
+    const int slices = W4S_MMA_WARPS >> a.lg, group = warp & ((1 << a.lg) - 1), slice = warp >> a.lg;
+    float acc[2][NB][4];
+#pragma unroll
+    for (int i = 0; i < 2 * NB * 4; ++i) acc[i / (4 * NB)][i / 4 % NB][i % 4] = 0.f;
+    W4Pos pos;
+    int q = 0, n_acc = 0;
+    bool ok = true;
+    // this lane's activations: of its rows in shared memory (from block 0), or of a fragment
+    uint32_t x0[NB];
+    const uint32_t x_half = a.frag ? NB * 512 : 64, x_block = a.frag ? FB : 128;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      x0[j] = a.frag ? 512 * j + 16 * lane
+                     : smem_u32(w4sm + SL.act) + min((lane >> 2) + 8 * j, a.T - 1) * (2 * a.K + 64) + 16 * (lane & 3);
+    for (; ok; ++n_acc) {
+      int u = -1, ns = 0;
+      for (int b = 0; b < blocks; b += a.step) {
+        if (sy.aborted() || !w4s_wait(sy.full(pos.s), pos.phase)) {
+          ok = false;
+          break;
+        }
+        if (b == 0) {
+          u = unit_ring[n_acc % W4S_UNITS];
+          if (u < 0) break;
+          ns = (MODE == W4_GEGLU ? 2 : 1) * strips_of(u);
+          if (n_acc == 0 && !a.frag && !w4s_wait(sy.act_full(), 0)) {
+            ok = false;
+            break;
+          }
+        }
+        if (warp == 0 && lane == 0) sy.flags[2] = q + 1;
+        ++q;
+        if (2 * group < ns) {
+          const int n = min(a.step, blocks - b);
+          // this warp's blocks: those whose place along K is `slice` modulo the slices
+          const int f = (slice - b) & (slices - 1);
+          const uint32_t st = smem_u32(w4sm) + pos.s * a.stage;
+          // a unit's odd last strip is multiplied twice; the second sum is not read
+          const uint32_t to1 = 2 * group + 1 < ns ? n * R : 0;
+          uint32_t xr[NB];
+#pragma unroll
+          for (int j = 0; j < NB; ++j) xr[j] = x0[j] + (a.frag ? st + ns * n * R + f * x_block : (b + f) * x_block);
+          w4s_blocks<NB, G32, ZP>(acc, (n - f + slices - 1) >> (3 - a.lg),
+                                  st + (2 * group * n + f) * R + 16 * lane, to1, slices * R, xr,
+                                  x_block * slices, x_half, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.empty(pos.s));
+        pos.next();
+      }
+      if (!ok) break;
+      const int buf = n_acc & 1;
+      if (n_acc >= 2 && !w4s_wait(sy.acc_empty(buf), ((n_acc >> 1) - 1) & 1)) {
+        ok = false;
         break;
       }
-      const int4 u = L.acc_unit[b];
-      if (u.x < 0) break;
-      const float* acc = L.acc + b * (w4s_acc_bytes<NB>() / 4);
-      if (MODE == W4_GEGLU) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-        for (int i = et; i < 16 * a.T; i += 32 * W4S_EPI_WARPS) {
-          const int r = i & 15, c = i >> 4;
-          const float gt = w4s_join<NB>(acc, u.w, 0, c, r), up = w4s_join<NB>(acc, u.w, 1, c, r);
-          out[(size_t)c * a.N + 16 * u.x + r] = __float2bfloat16_rn(w4_geglu(gt, up));
-        }
-      } else {
-        const int wide = 16 * u.y, n0 = (u.x << (a.lg + 1)) * W4_ROWS;
-        for (int c = 0; c < a.T; ++c)
-          for (int i = et; i < wide; i += 32 * W4S_EPI_WARPS) {
-            const float v = w4s_join<NB>(acc, u.w, i >> 4, c, i & 15);
-            const size_t o = (size_t)c * a.N + n0 + i;
+      if (warp == 0 && lane == 0) acc_unit[buf] = u;
+      if (u >= 0)
+        w4s_put<NB>(acc, smem_u32(w4sm + SL.acc) + buf * w4s_acc_bytes<NB>(), ((slice << a.lg) + group) * 2,
+                    lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sy.acc_full(buf));
+      if (u < 0) break;
+    }
+    if (!ok) sy.abort();
+  } else {
+    const int et = tid - 32 * W4S_MMA_WARPS;
+    if (a.early) pdl_wait();   // the outputs may be what the previous kernel still reads
+    for (int n = 0;; ++n) {
+      const int buf = n & 1;
+      if (sy.aborted() || !w4s_wait(sy.acc_full(buf), (n >> 1) & 1)) {
+        sy.abort();
+        break;
+      }
+      const int u = acc_unit[buf];
+      if (u < 0) break;
+      const float* acc = reinterpret_cast<const float*>(w4sm + SL.acc) + buf * (w4s_acc_bytes<NB>() / 4);
+      const int wide = 16 * strips_of(u);
+      for (int c = 0; c < a.T; ++c)
+        for (int i = et; i < wide; i += W4S_EPI_THREADS) {
+          if (MODE == W4_GEGLU) {
+            const float gt = w4s_join<NB>(acc, a.lg, 2 * (i >> 4), c, i & 15);
+            const float up = w4s_join<NB>(acc, a.lg, 2 * (i >> 4) + 1, c, i & 15);
+            const int f = (16 << a.lg) * u + i;
+            const size_t o = a.out_frag ? w4_frag_index(a.out_frag, c, f) : (size_t)c * a.N + f;
+            static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(w4_geglu(gt, up));
+          } else {
+            const float v = w4s_join<NB>(acc, a.lg, i >> 4, c, i & 15);
+            const size_t o = (size_t)c * a.N + (32 << a.lg) * (size_t)u + i;
             if (MODE == W4_LINEAR_F32) static_cast<float*>(a.out)[o] = v;
             else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
           }
-      }
+        }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.acc_empty(b));
+      if (lane == 0) mbar_arrive(sy.acc_empty(buf));
     }
   }
   __syncthreads();
-  if (*reinterpret_cast<volatile int*>(L.abort_flag) && tid == 0) w4s_drain<NB>(L);
+  if (sy.aborted() && tid == 0) sy.drain();
 }
 
 }  // namespace moe

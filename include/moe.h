@@ -378,9 +378,12 @@ moe_status_t moe_w4_dequantize_weights(const void *packed, int E, int K, int N, 
                                        unsigned flags, void *w, void *stream);
 
 /* y = x W for 0 <= T <= 16 rows: x bf16 [T, K], w packed (E = 1), y bf16 [T, N], or fp32 with
- * MOE_FLAG_F32_OUT (logits).  x, w and y 16-byte aligned; y may not alias x.  No workspace. */
+ * MOE_FLAG_F32_OUT (logits).  x, w, y and workspace 16-byte aligned; y may not alias x.
+ * Workspace: moe_linear_w4_workspace_size bytes; 0 bytes (small T K) need none, and NULL will do. */
+size_t moe_linear_w4_workspace_size(int T, int K);
 moe_status_t moe_linear_w4(const void *x, const void *w, int T, int K, int N, int group,
-                           unsigned flags, void *y, void *stream);
+                           unsigned flags, void *y, void *workspace, size_t workspace_bytes,
+                           void *stream);
 
 /* The dense GEGLU MLP of moe_dense_ffn with 4-bit weights, T <= 16: w_gate, w_up packed (K = H,
  * N = I), w_down packed (K = I, N = H).  h is rounded to bf16 between the two products, as in

@@ -87,12 +87,20 @@ def test_weight_calls_refuse(lib):
 
 def test_linear_refuses(lib):
     f = lib.moe_linear_w4
-    ok = dict(x=FAKE, w=FAKE, T=8, K=128, N=64, group=64, flags=0, y=FAKE + 4096)
+    ws = lib.moe_linear_w4_workspace_size
+    assert ws(1, 2816) == 0 and ws(8, 128) == 0                # kept in shared memory
+    assert ws(16, 2816) >= 2 * 16 * 2816 and ws(8, 16384) >= 2 * 8 * 16384
+    assert ws(0, 128) == 0 and ws(17, 128) == 0 and ws(8, 100) == 0
+    ok = dict(x=FAKE, w=FAKE, T=8, K=128, N=64, group=64, flags=0, y=FAKE + 4096, ws=None, n=0)
 
     def rc(**kw):
         a = {**ok, **kw}
-        return f(a["x"], a["w"], a["T"], a["K"], a["N"], a["group"], a["flags"], a["y"], None)
+        return f(a["x"], a["w"], a["T"], a["K"], a["N"], a["group"], a["flags"], a["y"], a["ws"],
+                 a["n"], None)
     assert rc(T=0) == 0
+    assert rc(T=16, K=4096) == _abi.MOE_ERR_INVALID_ARG         # needs a workspace
+    assert rc(T=16, K=4096, ws=FAKE + 8, n=1 << 30) == _abi.MOE_ERR_INVALID_ARG
+    assert rc(T=16, K=4096, ws=FAKE, n=1024) == _abi.MOE_ERR_NO_WORKSPACE
     for kw in (dict(x=None), dict(w=None), dict(y=None), dict(x=FAKE + 2), dict(w=FAKE + 8),
                dict(y=FAKE + 4), dict(y=FAKE), dict(T=-1), dict(group=16), dict(flags=1),
                dict(K=0), dict(N=-16)):
