@@ -389,7 +389,7 @@ moe_status_t moe_forward_w4(const void* x, const void* w_router, const float* ro
   a.y = static_cast<__nv_bfloat16*>(y);
   const Launch launch{static_cast<cudaStream_t>(stream), true};
   launch(true, w4_front_kernel, dim3(W.slices, (T + W4M_TT - 1) / W4M_TT), dim3(W4M_FRONT_THREADS), 0, a.x,
-         a.wr, T, H, E, logit, xn2, wn2, a.ctr, W.n_ctr, a.stats);
+         a.wr, T, H, E, logit, xn2, wn2, a.ctr, W.n_ctr, a.stats, a.ids, k);
   if (const moe_status_t s = launched(); s != MOE_OK) return s;
   w4_by_form(T, group, flags & MOE_FLAG_W4_ZEROS, [&](auto nb, auto g32, auto zp) {
     constexpr int NB = decltype(nb)::value;

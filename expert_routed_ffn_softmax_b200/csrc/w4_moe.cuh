@@ -35,7 +35,8 @@ constexpr int W4M_TT = 4;
 __global__ void __launch_bounds__(W4M_FRONT_THREADS) w4_front_kernel(
     const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wr, int T, int H, int E,
     double* __restrict__ part_logit, double* __restrict__ part_xn2, double* __restrict__ part_wn2,
-    int* __restrict__ counters, int n_counters, unsigned* __restrict__ stats) {
+    int* __restrict__ counters, int n_counters, unsigned* __restrict__ stats, int32_t* __restrict__ ids,
+    int k) {
   constexpr int TT = W4M_TT;
   pdl_wait();
   pdl_trigger();
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(W4M_FRONT_THREADS) w4_front_kernel(
     for (int i = s * W4M_FRONT_THREADS + tid; i < n_counters; i += gridDim.x * W4M_FRONT_THREADS)
       counters[i] = 0;
     if (s == 0 && tid < 5) stats[tid] = 0;
+    if (s == 0 && tid < T * k) ids[tid] = -1;   // not selected yet
   }
   const int pairs = E / 2, groups = W4M_FRONT_THREADS / pairs;   // E % 4 == 0, E <= 256
   const int ep = tid % pairs, grp = tid / pairs;
@@ -119,6 +121,7 @@ __global__ void __launch_bounds__(W4M_FRONT_THREADS) w4_front_kernel(
     if (lane == 0) part_xn2[(size_t)s * T + t0 + t] = v;
   }
 }
+static_assert(W4S_EPI_WARPS == 2, "one joining warp per accumulator tile");
 static_assert(W4M_TT * W4M_SLICE == W4M_FRONT_THREADS, "one activation per thread");
 
 // ----------------------------------------------------------------------------- the layer
@@ -134,15 +137,15 @@ struct W4Moe {
   float* wts;
   unsigned* stats;
   int32_t *counts, *offsets, *perm; // optional outputs
-  // counters, zeroed by the front kernel: {next token to select, tokens with ids, next unit, tokens
-  // with weights, GEMM-1 units joined (x joining warps)},
+  // counters, zeroed by the front kernel: {-, -, next unit, tokens with weights, GEMM-1 units
+  // joined, ...}, claimed [16] per token,
   // h_ready [128] per active expert, o_ready [row blocks of W_down]
   int* ctr;
   __nv_bfloat16* h;                 // [T k][I]
   float* o;                         // [T k][H]: expert outputs
   __nv_bfloat16* y;
 };
-constexpr int W4M_CTR_H = 8, W4M_CTR_O = W4M_CTR_H + W4M_MAX_PAIRS;
+constexpr int W4M_CTR_CLAIM = 8, W4M_CTR_H = W4M_CTR_CLAIM + W4_MAX_T, W4M_CTR_O = W4M_CTR_H + W4M_MAX_PAIRS;
 
 // Wait until *p >= target (another CTA's release), polling without a pause: these hand-overs are
 // on the layer's critical path.
@@ -183,7 +186,7 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
   double* sSelV = sB + 256;                          // [8]
   double* sSelB = sSelV + 8;                         // [8]
   int* sSelE = reinterpret_cast<int*>(sSelB + 8);    // [8]
-  double* sNorm = sSelB + 16;                        // [2] |x_t|^2, bound of |w_e|^2
+  double* sNorm = sSelB + 16;                        // [1] rounding bound without the bias
   double* sPart = sSelB + 24;                        // [W4S_THREADS]
   unsigned long long* sKey = reinterpret_cast<unsigned long long*>(sPart + W4S_THREADS);   // [256]
   int* sRank = reinterpret_cast<int*>(sKey + 256);            // [256]
@@ -203,16 +206,18 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
     }
     sPart[tid] = v;
   }
-  if (warp >= WARPS - 2) {
-    // the last two warps also add the norms
-    const bool xn = warp == WARPS - 1;
-    const int n = xn ? a.slices : a.slices * (W4M_FRONT_THREADS / 32);
-    double v = 0.0;
-#pragma unroll 8
-    for (int s = lane; s < n; s += 32) v += __ldcg(xn ? a.part_xn2 + (size_t)s * a.T + t : a.part_wn2 + s);
+  if (warp == WARPS - 1) {
+    // the last warp also adds the norms: |x_t|^2 and the bound of every |w_e|^2
+    double v = 0.0, w2 = 0.0;
+    for (int s = lane; s < a.slices; s += 32) v += __ldcg(a.part_xn2 + (size_t)s * a.T + t);
+#pragma unroll 4
+    for (int s = lane; s < a.slices * (W4M_FRONT_THREADS / 32); s += 32) w2 += __ldcg(a.part_wn2 + s);
 #pragma unroll
-    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (lane == 0) sNorm[xn ? 0 : 1] = v;
+    for (int off = 16; off; off >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, off);
+      w2 += __shfl_xor_sync(0xffffffffu, w2, off);
+    }
+    if (lane == 0) *sNorm = a.beta_scale * sqrt(v * w2) * (1.0 + 1e-6);
   }
   __syncthreads();
   if (tid < E) {
@@ -221,7 +226,7 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
     const double b = a.bias ? (double)a.bias[tid] : 0.0;
     if (a.bias) v += b;
     sL[tid] = v;
-    sB[tid] = a.beta_scale * (sqrt(sNorm[0] * sNorm[1]) * (1.0 + 1e-6) + fabs(b));
+    sB[tid] = *sNorm + a.beta_scale * fabs(b);
     // an unsigned key in the logits' order (-0 as 0, NaN below every number)
     const long long bits = __double_as_longlong(v + 0.0);
     sKey[tid] = isnan(v) ? 1ull : (unsigned long long)(bits ^ ((bits >> 63) | (1ll << 63)));
@@ -231,10 +236,14 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
   // rank of expert e by (logit desc, id asc): each group of threads counts over a part of the ids
   if (grp < groups) {
     const unsigned long long mine = sKey[e];
-    const int lo = grp * E / groups, hi = (grp + 1) * E / groups;
+    const int lo = (grp * (E / 2) / groups) * 2, hi = ((grp + 1) * (E / 2) / groups) * 2;   // E is even
     int r = 0;
 #pragma unroll 4
-    for (int x = lo; x < hi; ++x) r += sKey[x] > mine - (x < e ? 1 : 0);
+    for (int x = lo; x < hi; x += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(sKey + x);
+      r += two.x > mine - (x < e ? 1 : 0);
+      r += two.y > mine - (x + 1 < e ? 1 : 0);
+    }
     if (r) atomicAdd(&sRank[e], r);
   }
   __syncthreads();
@@ -253,13 +262,9 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
   if (tid < 32) {
     if (!ok) {
       w4_exact_token(sL, sB, t, a, sPart);
-      __syncwarp();
-      if (lane == 0) red_release_add_gpu(a.ctr + 1, 1);
     } else {
-      // the ids at once, for the CTAs that wait to stream; the weights are needed last
-      if (lane < a.k) a.ids[(size_t)t * a.k + lane] = sSelE[lane];
-      __syncwarp();
-      if (lane == 0) red_release_add_gpu(a.ctr + 1, 1);
+      // the ids at once: other CTAs poll them to start their streams; the weights are needed last
+      if (lane < a.k) *reinterpret_cast<volatile int32_t*>(a.ids + (size_t)t * a.k + lane) = sSelE[lane];
       // The differences are taken in fp64; their exponentials and the sum in fp32 (the weights are
       // fp32: off by 2^-24 |difference| plus a few 2^-24).  The fp64 exp's code alone, fetched
       // cold once a launch, took 3 us.
@@ -291,13 +296,12 @@ struct W4List {
   int* info;    // {active experts}
 };
 
-// sIds: scratch of W4M_MAX_PAIRS + 8 ints, 16-byte aligned.
+// sIds: the ids of all pairs (past T k: larger than any), then 8 ints of scratch; 16-byte aligned.
 __device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, int* sIds, int stage,
                                                 int record) {
   const int tid = threadIdx.x, P = a.T * a.k;
   unsigned* sMask = reinterpret_cast<unsigned*>(sIds + W4M_MAX_PAIRS);   // active experts, one bit each
-  const int id = tid < P ? __ldcg(a.ids + tid) : 0x7fffffff;
-  if (tid < W4M_MAX_PAIRS) sIds[tid] = id;
+  const int id = tid < W4M_MAX_PAIRS ? sIds[tid] : 0x7fffffff;
   if (tid < 8) sMask[tid] = 0;
   __syncthreads();
   int before = 0, same = 0;
@@ -400,27 +404,44 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
   list.expert = list.pair + 2 * W4M_MAX_PAIRS;
   list.off = list.pair + 3 * W4M_MAX_PAIRS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) sy.reset();
+  if (tid == 0) sy.reset(1);
   pdl_wait();
   pdl_trigger();
-  // ---- selection: tokens are taken from a counter until none is left (at once, when an earlier
-  // launch's wait has run out)
-  bool dead = false;
+  // ---- selection: CTA t selects token t.  Every CTA then polls the ids themselves (-1 until they
+  // are there).  The CTAs wait for CTAs that may not have started, if other work holds the SMs: one
+  // that has waited long takes any token that nobody has claimed, so the wait ends.
+  int* sIds = reinterpret_cast<int*>(acc_tiles);   // scratch until the first unit is joined
+  const int P = a.T * a.k;
+  if (tid == 0) {
+    const bool dead = *reinterpret_cast<volatile unsigned*>(&g_error_word) & MOE_DEVERR_TIMEOUT;
+    *s_token = dead ? -1 : (int)blockIdx.x < a.T && !atomicExch(a.ctr + W4M_CTR_CLAIM + blockIdx.x, 1) ? (int)blockIdx.x
+                                                                                                   : a.T;
+  }
+  __syncthreads();
+  const uint64_t since = global_timer_ns();
   while (true) {
+    const int t = *s_token;
+    if (t < 0) return;   // an earlier launch's wait ran out, or this one's: nothing is in flight
+    if (t < a.T) w4_select(a, t, w4sm);
+    // wait a while for the ids
+    int id = tid < P ? -1 : 0x7fffffff;
+    const uint64_t t0 = global_timer_ns();
+    while (id < 0 && global_timer_ns() - t0 < 20000)
+      id = *reinterpret_cast<const volatile int32_t*>(a.ids + tid);
+    if (tid < W4M_MAX_PAIRS) sIds[tid] = id;
+    if (__syncthreads_and(id >= 0)) break;
     if (tid == 0) {
-      dead = *reinterpret_cast<volatile unsigned*>(&g_error_word) & MOE_DEVERR_TIMEOUT;
-      *s_token = dead ? a.T : atomicAdd(a.ctr, 1);
+      int next = a.T;
+      for (int i = 0; i < a.T && next == a.T; ++i)
+        if (!atomicExch(a.ctr + W4M_CTR_CLAIM + i, 1)) next = i;
+      if (next == a.T && global_timer_ns() - since > *reinterpret_cast<volatile unsigned long long*>(&g_wait_limit_ns)) {
+        raise_error(MOE_DEVERR_TIMEOUT);
+        next = -1;
+      }
+      *s_token = next;
     }
     __syncthreads();
-    const int t = *s_token;
-    __syncthreads();
-    if (t >= a.T) break;
-    w4_select(a, t, w4sm);
   }
-  if (tid == 0) *s_token = !dead && w4m_wait(a.ctr + 1, a.T);
-  __syncthreads();
-  if (!*s_token) return;   // nothing is in flight
-  int* sIds = reinterpret_cast<int*>(acc_tiles);   // scratch until the first unit is joined
   w4_build_lists(a, list, sIds, STAGE, R);
   if (blockIdx.x == 0 && (a.counts || a.offsets || a.perm)) {
     w4_write_aux(a, list, sIds);
@@ -508,8 +529,8 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
             pos.next();
           }
           if (ok && !all_h) {
-            ok = w4m_wait(h_ready + ai, W4S_EPI_WARPS * strips1);
-            all_h = ld_acquire_gpu(a.ctr + 4) == W4S_EPI_WARPS * U1;
+            ok = w4m_wait(h_ready + ai, strips1);
+            all_h = ld_acquire_gpu(a.ctr + 4) == U1;
           }
           fence_proxy_async_global();
           W4Pos p = from;
@@ -593,26 +614,36 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
         w4s_put<NB>(acc, smem_u32(acc_tiles) + buf * w4s_acc_bytes<NB>(), ((slice << lg) + group) * 2, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(sy.acc_full(buf));
-      if (unit < 0) break;
+      if (unit < 0) {
+        // the end, to the other joining warp too
+        const int last = buf ^ 1, m = n_unit + 1;
+        ok = m < 2 || w4s_wait(sy.acc_empty(last), ((m >> 1) - 1) & 1);
+        if (!ok) break;
+        if (warp == 0 && lane == 0) acc_unit[last] = make_int4(-1, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.acc_full(last));
+        break;
+      }
     }
     if (!ok) sy.abort();
   } else {
-    const int et = tid - 32 * W4S_MMA_WARPS;
+    // the joining warps take the units in turn, one accumulator tile each: publishing a unit's
+    // outputs takes a fence of almost a microsecond, which must not hold up the next unit
+    const int buf = warp - W4S_MMA_WARPS;
+    const float* acc = acc_tiles + buf * (w4s_acc_bytes<NB>() / 4);
     for (int n = 0;; ++n) {
-      const int buf = n & 1;
-      if (sy.aborted() || !w4s_wait(sy.acc_full(buf), (n >> 1) & 1)) {
+      if (sy.aborted() || !w4s_wait(sy.acc_full(buf), n & 1)) {
         sy.abort();
         break;
       }
       const int4 u = acc_unit[buf];
       if (u.x < 0) break;
-      const float* acc = acc_tiles + buf * (w4s_acc_bytes<NB>() / 4);
       bool down;
       int ai, blk;
       split(u.x, down, ai, blk);
       const int off = list.off[ai];
       if (!down) {
-        for (int i = et; i < 16 * u.z; i += W4S_EPI_THREADS) {
+        for (int i = lane; i < 16 * u.z; i += 32) {
           const int r = i & 15, c = i >> 4;
           const float gt = w4s_join<NB>(acc, 0, 0, c, r), up = w4s_join<NB>(acc, 0, 1, c, r);
           a.h[(size_t)list.pair[off + c] * a.I + 16 * blk + r] = __float2bfloat16_rn(w4_geglu(gt, up));
@@ -621,15 +652,16 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
         const int n0 = (blk << (a.lg2 + 1)) * W4_ROWS;
         for (int c = 0; c < u.z; ++c) {
           float* o = a.o + (size_t)list.pair[off + c] * a.H + n0;
-          for (int i = et; i < 16 * u.y; i += W4S_EPI_THREADS)
-            o[i] = w4s_join<NB>(acc, u.w, i >> 4, c, i & 15);
+#pragma unroll 2
+          for (int i = lane; i < 16 * u.y; i += 32) o[i] = w4s_join<NB>(acc, u.w, i >> 4, c, i & 15);
         }
       }
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(sy.acc_empty(buf));
-        red_release_add_gpu(down ? o_ready + blk : h_ready + ai, 1);
-        if (!down) red_release_add_gpu(a.ctr + 4, 1);
+        __threadfence();   // the warp's stores before either count
+        atomicAdd(down ? o_ready + blk : h_ready + ai, 1);
+        if (!down) atomicAdd(a.ctr + 4, 1);
       }
     }
   }
@@ -644,7 +676,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
   const int share = (items + gridDim.x - 1) / gridDim.x;
   for (int i = blockIdx.x * share + tid; i < min(items, (int)(blockIdx.x + 1) * share); i += W4S_THREADS) {
     const int t = i / quads, n = 4 * (i - t * quads);
-    if (!w4m_wait(o_ready + (n / W4_ROWS >> (a.lg2 + 1)), W4S_EPI_WARPS * n_act) || !w4m_wait(a.ctr + 3, a.T))
+    if (!w4m_wait(o_ready + (n / W4_ROWS >> (a.lg2 + 1)), n_act) || !w4m_wait(a.ctr + 3, a.T))
       return;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < a.k; ++j) {

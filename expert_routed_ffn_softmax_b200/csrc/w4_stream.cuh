@@ -78,14 +78,15 @@ struct W4Sync {
     base = smem_u32(at);
     flags = reinterpret_cast<volatile int*>(at + 8 * (2 * W4S_STAGES + 6));
   }
-  __device__ void reset() const {
+  // joiners: joining warps that release an accumulator tile
+  __device__ void reset(int joiners) const {
     for (int s = 0; s < W4S_STAGES; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), W4S_MMA_WARPS);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), W4S_MMA_WARPS);
-      mbar_init(acc_empty(b), W4S_EPI_WARPS);
+      mbar_init(acc_empty(b), joiners);
     }
     mbar_init(act_full(), 1);
     mbar_init(steal_full(), 1);
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
   W4Sync sy;
   sy.init(w4sm + SL.sync);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) sy.reset();
+  if (tid == 0) sy.reset(W4S_EPI_WARPS);
   if (!a.early) {
     pdl_wait();
     pdl_trigger();
