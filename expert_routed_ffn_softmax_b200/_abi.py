@@ -8,7 +8,6 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -476,11 +475,12 @@ class W4Weights:
     """E matrices [K, N] as packed 4-bit codes with group scales (and zero points): the layout of
     include/moe.h in ``data`` (uint8 [E, N/16, K/64, R], CUDA).  Made by w4_pack or w4_quantize."""
 
-    __slots__ = ("data", "E", "K", "N", "group", "zeros", "flags")
+    __slots__ = ("data", "E", "K", "N", "group", "zeros", "flags", "index")
 
     def __init__(self, data: torch.Tensor, E: int, K: int, N: int, group: int, zeros: bool):
         self.data, self.E, self.K, self.N, self.group, self.zeros = data, E, K, N, group, zeros
         self.flags = MOE_FLAG_W4_ZEROS if zeros else 0
+        self.index = data.get_device()
 
     @property
     def shape(self) -> tuple[int, int, int]:
@@ -495,39 +495,62 @@ class W4Weights:
                 f"zeros={self.zeros}, device={self.device})")
 
 
-def _on_device(fn):
-    """Run a call on its first argument's device and on `stream` (default: that device's current
-    one), so that memory the call allocates belongs to the stream that its kernels run on."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        t = first.data if isinstance(first, W4Weights) else first
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError("the first argument must be a CUDA tensor or W4Weights")
-        if stream is None and t.device.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
-        with torch.cuda.device(t.device):
-            with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
-                if torch.cuda.current_device() != t.device.index:
-                    raise ValueError("stream belongs to another device than the tensors")
-                return fn(first, *args, **kw)
-    return call
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else \
+    torch.cuda.current_device
 
 
-def _same(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> int:
-    p = _dev(t, name, dtype, shape)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _raw_stream(index: int) -> int:
+    """The device's current stream as an integer (the calls below last a few microseconds, so the
+    way to it is short)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _elsewhere(fn, first, stream, args):
+    """Run fn(*args) on `first`'s device and on `stream` (default: that device's current one), so
+    that what the call allocates belongs to the stream that its kernels run on."""
+    t = first.data if isinstance(first, W4Weights) else first
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("the first argument must be a CUDA tensor or W4Weights")
+    with torch.cuda.device(t.device):
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+            if torch.cuda.current_device() != t.device.index:
+                raise ValueError("stream belongs to another device than the tensors")
+            return fn(*args)
+
+
+def _here(first) -> bool:
+    """Whether the tensor is on the current device."""
+    return first.get_device() == _current_device()
+
+
+def _tensor(t, name: str, dtype: torch.dtype, shape: tuple, index: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device `index`."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    p = _dev(t, name, dtype, shape)      # says what is wrong
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     return p
 
 
-def _w4(w: W4Weights, name: str, E: int, K: int, N: int, dev: torch.device) -> int:
-    if not isinstance(w, W4Weights):
+def _w4(w, name: str, E: int, K: int, N: int, index: int) -> int:
+    if type(w) is not W4Weights:
         raise TypeError(f"{name} must be W4Weights (w4_pack, w4_quantize)")
     if w.E != E or w.K != K or w.N != N:
         raise ValueError(f"{name} must hold {E} matrices of [{K}, {N}], got {w}")
-    if w.data.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {w.data.device}")
+    if w.index != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {w.device}")
     return w.data.data_ptr()
+
+
+def _rows(x, name: str):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(x.shape)}")
+    return x.shape
 
 
 def _w4_empty(E: int, K: int, N: int, group: int, zeros: bool, dev) -> W4Weights:
@@ -535,183 +558,195 @@ def _w4_empty(E: int, K: int, N: int, group: int, zeros: bool, dev) -> W4Weights
     if n == 0:
         raise MoEError(MOE_ERR_UNSUPPORTED if group in (32, 64, 128) else MOE_ERR_INVALID_ARG,
                        "moe_w4_packed_bytes")
-    data = torch.empty((E, N // 16, K // 64, n // (E * (N // 16) * (K // 64))), dtype=torch.uint8,
-                       device=dev)
+    data = torch.empty((E, N // 16, K // 64, n // (E * (N // 16) * (K // 64))), dtype=_U8, device=dev)
     return W4Weights(data, E, K, N, group, zeros)
 
 
-def _raw_stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-@_on_device
 def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
-            group: int = 64) -> W4Weights:
+            group: int = 64, stream=None) -> W4Weights:
     """moe_w4_pack: a checkpoint's 4-bit matrices -> W4Weights.  codes uint8 [E, N, K/2] (element
     2b in the low nibble of byte b), scales bf16 [E, N, ceil(K/group)], zeros uint8 of the same
     shape or None (symmetric, zero point 8); one matrix may leave E out."""
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        raise TypeError("codes must be a CUDA tensor")
+    if stream is not None or not _here(codes):
+        return _elsewhere(w4_pack, codes, stream, (codes, scales, zeros, group))
     if codes.dim() == 2:
         codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
         zeros = None if zeros is None else zeros.unsqueeze(0)
     if codes.dim() != 3:
         raise ValueError(f"codes must be [E, N, K/2] or [N, K/2], got {tuple(codes.shape)}")
     E, N, half = codes.shape
-    K, dev = 2 * half, codes.device
-    w = _w4_empty(E, K, N, group, zeros is not None, dev)
+    K, dev = 2 * half, codes.get_device()
+    w = _w4_empty(E, K, N, group, zeros is not None, codes.device)
     G = -(-K // group)
-    pc = _same(codes, "codes", torch.uint8, (E, N, half), dev)
-    ps = _same(scales, "scales", torch.bfloat16, (E, N, G), dev)
-    pz = None if zeros is None else _same(zeros, "zeros", torch.uint8, (E, N, G), dev)
+    pc = _tensor(codes, "codes", _U8, (E, N, half), dev)
+    ps = _tensor(scales, "scales", _BF16, (E, N, G), dev)
+    pz = None if zeros is None else _tensor(zeros, "zeros", _U8, (E, N, G), dev)
     _check(load().moe_w4_pack(pc, ps, pz, E, K, N, group, w.data.data_ptr(), _raw_stream(dev)),
            "moe_w4_pack")
     return w
 
 
-@_on_device
-def w4_quantize(w: torch.Tensor, group: int = 64, zeros: bool = False) -> W4Weights:
+def w4_quantize(w: torch.Tensor, group: int = 64, zeros: bool = False, stream=None) -> W4Weights:
     """moe_w4_quantize_weights: bf16 w [E, K, N] or [K, N] (N contiguous) -> W4Weights, symmetric
     or (zeros=True) with a zero point per group."""
+    if not isinstance(w, torch.Tensor) or not w.is_cuda:
+        raise TypeError("w must be a CUDA tensor")
+    if stream is not None or not _here(w):
+        return _elsewhere(w4_quantize, w, stream, (w, group, zeros))
     if w.dim() == 2:
         w = w.unsqueeze(0)
     if w.dim() != 3:
         raise ValueError(f"w must be [E, K, N] or [K, N], got {tuple(w.shape)}")
     E, K, N = w.shape
-    dev = w.device
-    pw = _same(w, "w", torch.bfloat16, (E, K, N), dev)
-    q = _w4_empty(E, K, N, group, zeros, dev)
+    dev = w.get_device()
+    pw = _tensor(w, "w", _BF16, (E, K, N), dev)
+    q = _w4_empty(E, K, N, group, zeros, w.device)
     _check(load().moe_w4_quantize_weights(pw, E, K, N, group, q.flags, q.data.data_ptr(),
                                           _raw_stream(dev)), "moe_w4_quantize_weights")
     return q
 
 
-@_on_device
-def w4_dequantize(w: W4Weights, out: torch.Tensor | None = None) -> torch.Tensor:
+def w4_dequantize(w: W4Weights, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """moe_w4_dequantize_weights: the bf16 weights [E, K, N] that w stands for (what forward and
     dense_ffn take for larger batches)."""
-    if not isinstance(w, W4Weights):
-        raise TypeError("w must be W4Weights (w4_pack, w4_quantize)")
-    dev = w.data.device
-    o = torch.empty(w.shape, dtype=torch.bfloat16, device=dev) if out is None else out
-    po = _same(o, "out", torch.bfloat16, w.shape, dev)
+    if type(w) is not W4Weights:
+        raise TypeError("w must be W4Weights on a CUDA device (w4_pack, w4_quantize)")
+    if stream is not None or w.index != _current_device():
+        return _elsewhere(w4_dequantize, w, stream, (w, out))
+    o = torch.empty(w.shape, dtype=_BF16, device=w.data.device) if out is None else out
+    po = _tensor(o, "out", _BF16, w.shape, w.index)
     _check(load().moe_w4_dequantize_weights(w.data.data_ptr(), w.E, w.K, w.N, w.group, w.flags, po,
-                                            _raw_stream(dev)), "moe_w4_dequantize_weights")
+                                            _raw_stream(w.index)), "moe_w4_dequantize_weights")
     return o
 
 
-@_on_device
-def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None,
-              fp32: bool = False, workspace_buf: torch.Tensor | None = None) -> torch.Tensor:
-    """moe_linear_w4: y = x W for x bf16 [T, K], T <= 16, and one 4-bit matrix -> y [T, N], bf16
-    (or fp32 with fp32=True).  stream=: run on that stream."""
-    if not isinstance(w, W4Weights):
-        raise TypeError("w must be W4Weights (w4_pack, w4_quantize)")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
-    T, K = x.shape
-    dev = x.device
-    px = _dev(x, "x", torch.bfloat16, (T, w.K))
-    pw = _w4(w, "w", 1, K, w.N, dev)
-    dt = torch.float32 if fp32 else torch.bfloat16
-    if out is None:
-        out = torch.empty((T, w.N), dtype=dt, device=dev)
-        py = out.data_ptr()
-    else:
-        py = _same(out, "out", dt, (T, w.N), dev)
-    if T:
-        L = load()
-        n = L.moe_linear_w4_workspace_size(T, K)
-        if n == 0:
-            pws = 0
-        else:
-            ws = _w4_workspace(n, workspace_buf, "", dev)
-            pws, n = ws.data_ptr(), ws.numel()
-        _check(L.moe_linear_w4(px, pw, T, K, w.N, w.group,
-                               w.flags | (MOE_FLAG_F32_OUT if fp32 else 0), py, pws, n,
-                               _raw_stream(dev)), "moe_linear_w4")
-    return out
-
-
-def _w4_workspace(nbytes: int, given: torch.Tensor | None, what: str, dev) -> torch.Tensor:
-    """The call's own scratch (torch's allocator ties it to the current stream, or to the graph
-    being captured, so calls on other streams and other graphs never share it), or the caller's."""
+def _w4_workspace(nbytes: int, given: torch.Tensor | None, what: str, x) -> tuple[int, int, object]:
+    """Address, bytes and owner of a call's scratch: the caller's, or memory of its own (torch's
+    allocator ties it to the current stream, or to the graph being captured, so calls on other
+    streams and other graphs never share it)."""
     if nbytes == 0:
         raise MoEError(MOE_ERR_UNSUPPORTED, what)
     if given is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _same(given, "workspace_buf", torch.uint8, (given.numel(),), dev)
-    return given
+        given = torch.empty(nbytes, dtype=_U8, device=x.device)
+        return given.data_ptr(), nbytes, given
+    n = given.numel()
+    return _tensor(given, "workspace_buf", _U8, (n,), x.get_device()), n, given
 
 
-def _w4_same_form(*ws: W4Weights) -> None:
-    if any(w.group != ws[0].group or w.zeros != ws[0].zeros for w in ws):
+def _w4_same_form(a: W4Weights, b: W4Weights, c: W4Weights) -> None:
+    if a.group != b.group or a.group != c.group or a.zeros != b.zeros or a.zeros != c.zeros:
         raise ValueError("the matrices of one layer must share group and zeros")
 
 
-@_on_device
+def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, fp32: bool = False,
+              workspace_buf: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """moe_linear_w4: y = x W for x bf16 [T, K], T <= 16, and one 4-bit matrix -> y [T, N], bf16
+    (or fp32 with fp32=True).  stream: run on that stream instead of the current one."""
+    T, K = _rows(x, "x")
+    if stream is not None or not _here(x):
+        return _elsewhere(linear_w4, x, stream, (x, w, out, fp32, workspace_buf))
+    dev = x.get_device()
+    N = w.N if type(w) is W4Weights else 0
+    pw = _w4(w, "w", 1, K, N, dev)
+    px = _tensor(x, "x", _BF16, (T, K), dev)
+    dt = _F32 if fp32 else _BF16
+    if out is None:
+        out = torch.empty((T, N), dtype=dt, device=x.device)
+        py = out.data_ptr()
+    else:
+        py = _tensor(out, "out", dt, (T, N), dev)
+    if T == 0:
+        return out
+    L = _lib or load()
+    pws = n = 0
+    if T * K >= _W4_WORKSPACE_FROM:
+        n = L.moe_linear_w4_workspace_size(T, K)
+        if n:
+            pws, n, _own = _w4_workspace(n, workspace_buf, "", x)
+    rc = L.moe_linear_w4(px, pw, T, K, N, w.group, w.flags | MOE_FLAG_F32_OUT if fp32 else w.flags, py,
+                         pws, n, _raw_stream(dev))
+    if rc:
+        _check(rc, "moe_linear_w4")
+    return out
+
+
+# moe_linear_w4_workspace_size is 0 for fewer elements (and T <= 8)
+_W4_WORKSPACE_FROM = 512
+
+
 def dense_ffn_w4(x: torch.Tensor, w_gate: W4Weights, w_up: W4Weights, w_down: W4Weights,
-                 out: torch.Tensor | None = None,
-                 workspace_buf: torch.Tensor | None = None) -> torch.Tensor:
+                 out: torch.Tensor | None = None, workspace_buf: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
     """moe_dense_ffn_w4: dense_ffn with 4-bit weights for T <= 16 tokens -> y bf16 [T, H]:
-    y = (gelu_tanh(x W_gate) * (x W_up)) W_down.  stream=: run on that stream."""
-    if x.dim() != 2:
-        raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
-    T, H = x.shape
-    dev = x.device
-    if not isinstance(w_gate, W4Weights):
-        raise TypeError("w_gate must be W4Weights (w4_pack, w4_quantize)")
-    I = w_gate.N
-    px = _dev(x, "x", torch.bfloat16, (T, H))
+    y = (gelu_tanh(x W_gate) * (x W_up)) W_down.  stream: run on that stream instead of the current
+    one."""
+    T, H = _rows(x, "x")
+    if stream is not None or not _here(x):
+        return _elsewhere(dense_ffn_w4, x, stream, (x, w_gate, w_up, w_down, out, workspace_buf))
+    dev = x.get_device()
+    I = w_gate.N if type(w_gate) is W4Weights else 0
     pg = _w4(w_gate, "w_gate", 1, H, I, dev)
     pu = _w4(w_up, "w_up", 1, H, I, dev)
     pd = _w4(w_down, "w_down", 1, I, H, dev)
     _w4_same_form(w_gate, w_up, w_down)
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
-    py = _same(y, "out", torch.bfloat16, (T, H), dev)
+    px = _tensor(x, "x", _BF16, (T, H), dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=_BF16, device=x.device)
+        py = out.data_ptr()
+    else:
+        py = _tensor(out, "out", _BF16, (T, H), dev)
     if T == 0:
-        return y
-    L = load()
-    ws = _w4_workspace(L.moe_dense_w4_workspace_size(T, H, I), workspace_buf,
-                       "moe_dense_w4_workspace_size", dev)
-    _check(L.moe_dense_ffn_w4(px, pg, pu, pd, T, H, I, w_gate.group, w_gate.flags, py,
-                              ws.data_ptr(), ws.numel(), _raw_stream(dev)), "moe_dense_ffn_w4")
-    return y
+        return out
+    L = _lib or load()
+    pws, n, _own = _w4_workspace(L.moe_dense_w4_workspace_size(T, H, I), workspace_buf,
+                                 "moe_dense_w4_workspace_size", x)
+    rc = L.moe_dense_ffn_w4(px, pg, pu, pd, T, H, I, w_gate.group, w_gate.flags, py, pws, n,
+                            _raw_stream(dev))
+    if rc:
+        _check(rc, "moe_dense_ffn_w4")
+    return out
 
 
-@_on_device
 def forward_w4(x: torch.Tensor, w_router: torch.Tensor, w_gate: W4Weights, w_up: W4Weights,
                w_down: W4Weights, k: int, bias: torch.Tensor | None = None, renorm: bool = True,
                aux: bool = False, out: torch.Tensor | None = None,
-               workspace_buf: torch.Tensor | None = None):
+               workspace_buf: torch.Tensor | None = None, stream=None):
     """moe_forward_w4: the routed layer with 4-bit expert weights for T <= 16 tokens -> y bf16
-    [T, H] (and the routing dict of forward if aux).  stream=: run on that stream."""
-    if x.dim() != 2 or w_router.dim() != 2:
-        raise ValueError("x must be [T, H] and w_router [H, E]")
-    T, H = x.shape
-    E = w_router.shape[1]
-    dev = x.device
-    if not isinstance(w_gate, W4Weights):
-        raise TypeError("w_gate must be W4Weights (w4_pack, w4_quantize)")
-    I = w_gate.N
-    px = _dev(x, "x", torch.bfloat16, (T, H))
-    pr = _same(w_router, "w_router", torch.bfloat16, (H, E), dev)
-    pb = None if bias is None else _same(bias, "bias", torch.float32, (E,), dev)
+    [T, H] (and the routing dict of forward if aux).  stream: run on that stream instead of the
+    current one."""
+    T, H = _rows(x, "x")
+    if stream is not None or not _here(x):
+        return _elsewhere(forward_w4, x, stream, (x, w_router, w_gate, w_up, w_down, k, bias, renorm,
+                                                  aux, out, workspace_buf))
+    E = _rows(w_router, "w_router")[1]
+    dev = x.get_device()
+    I = w_gate.N if type(w_gate) is W4Weights else 0
     pg = _w4(w_gate, "w_gate", E, H, I, dev)
     pu = _w4(w_up, "w_up", E, H, I, dev)
     pd = _w4(w_down, "w_down", E, I, H, dev)
     _w4_same_form(w_gate, w_up, w_down)
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
-    py = _same(y, "out", torch.bfloat16, (T, H), dev)
-    a, aux_d = _aux_out(T, E, k, dev) if aux else (None, None)
+    px = _tensor(x, "x", _BF16, (T, H), dev)
+    pr = _tensor(w_router, "w_router", _BF16, (H, E), dev)
+    pb = None if bias is None else _tensor(bias, "bias", _F32, (E,), dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=_BF16, device=x.device)
+        py = out.data_ptr()
+    else:
+        py = _tensor(out, "out", _BF16, (T, H), dev)
+    a, aux_d = _aux_out(T, E, k, x.device) if aux else (None, None)
     if T == 0:
-        return (y, aux_d) if aux else y
-    L = load()
-    flags = w_gate.flags | (0 if renorm else MOE_FLAG_NO_RENORM)
-    ws = _w4_workspace(L.moe_w4_workspace_size(T, H, E, I, k, flags), workspace_buf,
-                       "moe_w4_workspace_size", dev)
-    _check(L.moe_forward_w4(px, pr, pb, pg, pu, pd, T, H, E, I, k, w_gate.group, flags, py,
-                            None if a is None else ctypes.byref(a), ws.data_ptr(), ws.numel(),
-                            _raw_stream(dev)), "moe_forward_w4")
-    return (y, aux_d) if aux else y
+        return (out, aux_d) if aux else out
+    L = _lib or load()
+    flags = w_gate.flags if renorm else w_gate.flags | MOE_FLAG_NO_RENORM
+    pws, n, _own = _w4_workspace(L.moe_w4_workspace_size(T, H, E, I, k, flags), workspace_buf,
+                                 "moe_w4_workspace_size", x)
+    rc = L.moe_forward_w4(px, pr, pb, pg, pu, pd, T, H, E, I, k, w_gate.group, flags, py,
+                          None if a is None else ctypes.byref(a), pws, n, _raw_stream(dev))
+    if rc:
+        _check(rc, "moe_forward_w4")
+    return (out, aux_d) if aux else out
 
 
 def _aux_out(T: int, E: int, k: int, dev) -> tuple[AuxOut, dict]:

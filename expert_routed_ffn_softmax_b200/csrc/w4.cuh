@@ -111,46 +111,66 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
   w4_store_tile(rec, packed, e, n0, k0, K, N, R);
 }
 
+// A tile of bf16 weights in shared memory, [128 along K][64 rows], 8 elements of padding.
+constexpr int W4_TILE_PITCH = W4_TILE_N + 8;
+
+// rint(x / s) with the correctly rounded quotient; 0 for s = 0.  Out of line: rarely needed.
+__device__ __noinline__ float w4_rounded_quotient(float x, float s) {
+  return s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
+}
+
 // bf16 weights w [E][K][N] (N contiguous) -> packed.  Per group, in fp32, every step one
 // rounding to nearest even: symmetric scale = bf16(max |w| / 7), code = clamp(rint(w / scale)
 // + 8, 0, 15); asymmetric lo = min(w, 0), hi = max(w, 0), scale = bf16((hi - lo) / 15), zero =
 // clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15).  A zero scale
-// gives codes and zero points of 8.  Bound by its bytes (2.5 to 2.6 per weight).
+// gives codes and zero points of 8.  Bound by its bytes (2.5 to 2.6 per weight), so the tile comes
+// and goes in 16-byte vectors, and the division is a multiplication by the reciprocal: that is
+// within 2^-21 of the quotient (at most 16), so only where it lies closer than 2^-16 to the middle
+// between two integers can the rounded quotient be another one, and there it is divided.
 template <bool ZP>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K,
                                                           int N, int group,
                                                           uint8_t* __restrict__ packed) {
+  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
   __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
   __shared__ float s_lo[4][W4_TILE_N], s_hi[4][W4_TILE_N];
   const int R = w4_record(group, ZP), gpb = w4_groups(group);
   const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
+  const __nv_bfloat16* src = w + ((size_t)e * K + k0) * N + n0;
+#pragma unroll
+  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
+    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
+    if (k0 + k < K && n0 + 8 * v < N)
+      *reinterpret_cast<uint4*>(&tile[k][8 * v]) = __ldg(reinterpret_cast<const uint4*>(src + (size_t)k * N + 8 * v));
+  }
+  __syncthreads();
   const int row = threadIdx.x & 63, part = threadIdx.x >> 6;   // 32 elements of one row
-  const int n = n0 + row, k = k0 + 32 * part;
-  const bool in = n < N && k < K;
+  const bool in = n0 + row < N && k0 + 32 * part < K;
   float v[32];
   float lo = 0.f, hi = 0.f;
   if (in) {
-    const __nv_bfloat16* p = w + ((size_t)e * K + k) * N + n;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __bfloat162float(p[(size_t)i * N]);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
+      v[i] = __bfloat162float(tile[32 * part + i][row]);
       lo = fminf(lo, v[i]);
       hi = fmaxf(hi, v[i]);
     }
   }
-  s_lo[part][row] = lo;
-  s_hi[part][row] = hi;
-  __syncthreads();
-  if (in) {
+  if (group > 32) {
+    s_lo[part][row] = lo;
+    s_hi[part][row] = hi;
+    __syncthreads();
     const int span = group / 32, p0 = part / span * span;   // the 32-element parts of the group
     for (int i = p0; i < p0 + span; ++i) {
       lo = fminf(lo, s_lo[i][row]);
       hi = fmaxf(hi, s_hi[i][row]);
     }
+  }
+  if (in) {
     const __nv_bfloat16 sb = __float2bfloat16_rn(ZP ? __fdiv_rn(__fsub_rn(hi, lo), 15.f)
                                                     : __fdiv_rn(fmaxf(-lo, hi), 7.f));
-    const float s = __bfloat162float(sb);
+    const float s = __bfloat162float(sb), inv = __fdiv_rn(1.f, s);
+    const bool divide = !(s > 1e-30f && s < 1e30f);   // the reciprocal could leave the normal range
     const float z = ZP && s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 8.f;
     const int strip = row >> 4, r = row & 15, block = part >> 1, half = part & 1;
     uint8_t* b = rec + (strip * 2 + block) * R;
@@ -159,8 +179,10 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* _
       uint32_t word = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float q = s > 0.f ? rintf(__fdiv_rn(v[8 * t + j], s)) + z : z;
-        word |= (uint32_t)(int)fminf(fmaxf(q, 0.f), 15.f) << (4 * ((j >> 1) + 4 * (j & 1)));
+        const float x = v[8 * t + j], m = __fmul_rn(x, inv);
+        float q = rintf(m);
+        if (divide || fabsf(fabsf(m - q) - 0.5f) < 0x1p-16f) q = w4_rounded_quotient(x, s);
+        word |= (uint32_t)(int)fminf(fmaxf(q + z, 0.f), 15.f) << (4 * ((j >> 1) + 4 * (j & 1)));
       }
       *reinterpret_cast<uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half + 4 * (r >> 3)) = word;
     }
@@ -175,30 +197,46 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* _
 }
 
 // packed -> bf16 w [E][K][N]: each value rounded once (the difference of the codes is exact, its
-// product with the scale has at most 12 significant bits).
+// product with the scale has at most 12 significant bits).  Bound by its bytes, as above.
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __restrict__ packed, int K,
                                                             int N, int group, int zeros,
                                                             __nv_bfloat16* __restrict__ w) {
+  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
+  __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
   const int R = w4_record(group, zeros), gpb = w4_groups(group);
   const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
+  const int strips = min(4, (N - n0) / W4_ROWS), blocks = min(2, (K - k0) / W4_KB);
+  const int vec = blocks * R / 16;
+  for (int i = threadIdx.x; i < strips * vec; i += 256) {
+    const int s = i / vec, v = i - s * vec;
+    const uint8_t* src =
+        packed + (((size_t)e * (N / W4_ROWS) + n0 / W4_ROWS + s) * (K / W4_KB) + k0 / W4_KB) * R;
+    *reinterpret_cast<uint4*>(rec + s * 2 * R + 16 * v) = __ldg(reinterpret_cast<const uint4*>(src) + v);
+  }
+  __syncthreads();
   const int row = threadIdx.x & 63, part = threadIdx.x >> 6;
-  const int n = n0 + row, k = k0 + 32 * part;
-  if (n >= N || k >= K) return;
-  const int r = row & 15, half = part & 1;
-  const uint8_t* b = packed + (((size_t)e * (N / W4_ROWS) + n / W4_ROWS) * (K / W4_KB) + k / W4_KB) * R;
-  const int gi = half * (gpb - 1);
-  const float s = __bfloat162float(
-      reinterpret_cast<const __nv_bfloat16*>(b + 512)[gi * 16 + w4_row_slot(r)]);
-  const float z = zeros ? (float)b[512 + gpb * 32 + gi * 16 + w4_row_slot(r)] : 8.f;
-  __nv_bfloat16* p = w + ((size_t)e * K + k) * N + n;
+  if (row < 16 * strips && part < 2 * blocks) {
+    const int r = row & 15, half = part & 1, gi = half * (gpb - 1);
+    const uint8_t* b = rec + ((row >> 4) * 2 + (part >> 1)) * R;
+    const float s = __bfloat162float(
+        reinterpret_cast<const __nv_bfloat16*>(b + 512)[gi * 16 + w4_row_slot(r)]);
+    const float z = zeros ? (float)b[512 + gpb * 32 + gi * 16 + w4_row_slot(r)] : 8.f;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half +
-                                                             4 * (r >> 3));
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t word = *reinterpret_cast<const uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half +
+                                                               4 * (r >> 3));
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      p[(size_t)(8 * t + j) * N] =
-          __float2bfloat16_rn(__fmul_rn((float)w4_nibble(word, j) - z, s));
+      for (int j = 0; j < 8; ++j)
+        tile[32 * part + 8 * t + j][row] = __float2bfloat16_rn(__fmul_rn((float)w4_nibble(word, j) - z, s));
+    }
+  }
+  __syncthreads();
+  __nv_bfloat16* dst = w + ((size_t)e * K + k0) * N + n0;
+#pragma unroll
+  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
+    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
+    if (k0 + k < K && n0 + 8 * v < N)
+      *reinterpret_cast<uint4*>(dst + (size_t)k * N + 8 * v) = *reinterpret_cast<const uint4*>(&tile[k][8 * v]);
   }
 }
 
@@ -250,27 +288,11 @@ __device__ __forceinline__ W4Zero w4_zero(uint32_t zero) {
   return z;
 }
 
-// Reads at a 32-bit shared-memory address plus a constant (a generic pointer would cost a generic
-// load's address check, an added register an addition).
-template <int OFF>
-__device__ __forceinline__ uint4 lds_v4(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(at), "n"(OFF));
-  return v;
-}
-template <int OFF>
-__device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(v) : "r"(at), "n"(OFF));
-  return v;
-}
-template <int OFF>
-__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v) : "r"(at), "n"(OFF));
-  return v;
+// Reads at a 32-bit shared-memory address (the compiler sees the address space, so offsets fold
+// into the load).
+template <typename V>
+__device__ __forceinline__ V lds(uint32_t at) {
+  return *reinterpret_cast<const V*>(__cvta_shared_to_generic(at));
 }
 
 // acc[i][j] += block i * activation fragments, for the records of NS strips at the same place
@@ -288,7 +310,7 @@ __device__ __forceinline__ void w4_block(float (&acc)[NS][NB][4], const uint32_t
   uint32_t sc[NS], zp[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    q[i] = lds_v4<0>(rec[i]);
+    q[i] = lds<uint4>(rec[i]);
     sc[i] = rec[i] - 16 * lane + 4 * (lane >> 2);         // this lane's two rows' scales,
     if (ZP) zp[i] = rec[i] - 16 * lane + 2 * (lane >> 2);   // and zero points
   }
@@ -297,13 +319,13 @@ __device__ __forceinline__ void w4_block(float (&acc)[NS][NB][4], const uint32_t
   for (int h = 0; h < 2; ++h) {
     uint4 xf[NB];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) xf[j] = lds_v4<0>(h ? x[j] + x_half : x[j]);
+    for (int j = 0; j < NB; ++j) xf[j] = lds<uint4>(h ? x[j] + x_half : x[j]);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const uint32_t lo = h ? q[i].z : q[i].x, hi = h ? q[i].w : q[i].y;
       W4Zero z_lo = {0xC208C208u, 0xC000C000u}, z_hi = z_lo;   // zero points of 8
       if (ZP) {
-        const uint32_t two = G32 && h ? lds_u16<512 + GPB * 32 + 16>(zp[i]) : lds_u16<512 + GPB * 32>(zp[i]);
+        const uint32_t two = lds<uint16_t>(zp[i] + 512 + GPB * 32 + (G32 ? 16 * h : 0));
         z_lo = w4_zero(two & 0xffu);
         z_hi = w4_zero(two >> 8);
       }
@@ -318,7 +340,7 @@ __device__ __forceinline__ void w4_block(float (&acc)[NS][NB][4], const uint32_t
                  s == 0 && (G32 || h == 0));
       }
       if (G32 || h == 1) {
-        const uint32_t s2 = G32 && h ? lds_u32<512 + 32>(sc[i]) : lds_u32<512>(sc[i]);
+        const uint32_t s2 = lds<uint32_t>(sc[i] + 512 + (G32 ? 32 * h : 0));
         const float s_lo = __uint_as_float(s2 << 16), s_hi = __uint_as_float(s2 & 0xffff0000u);
 #pragma unroll
         for (int j = 0; j < NB; ++j) {

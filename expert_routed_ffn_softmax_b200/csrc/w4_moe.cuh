@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
         break;
       }
       const uint32_t head = smem_u32(descs + n_unit % W4M_DESCS);
-      const uint4 d0 = lds_v4<0>(head), d1 = lds_v4<16>(head);
+      const uint4 d0 = lds<uint4>(head), d1 = lds<uint4>(head + 16);
       const int unit = (int)d0.x, strips = d0.y, rows = d0.z, lg = d0.w, kb = d1.x, step = d1.y;
       const int slices = W4S_MMA_WARPS >> lg, group = warp & ((1 << lg) - 1), slice = warp >> lg;
       for (int b = 0; unit >= 0 && b < kb; b += step) {
