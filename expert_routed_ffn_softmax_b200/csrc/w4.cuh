@@ -51,10 +51,6 @@ __device__ __forceinline__ uint32_t w4_interleave(uint32_t w) {
   };
   return squeeze(w) | (squeeze(w >> 4) << 16);
 }
-// Nibble of element j (0..7) in a packed word.
-__device__ __forceinline__ uint32_t w4_nibble(uint32_t w, int j) {
-  return (w >> (4 * ((j >> 1) + 4 * (j & 1)))) & 15u;
-}
 // Position of row r (0..15) in a group's scales and zero points.
 __device__ __forceinline__ int w4_row_slot(int r) { return 2 * (r & 7) + (r >> 3); }
 
@@ -111,151 +107,6 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
   w4_store_tile(rec, packed, e, n0, k0, K, N, R);
 }
 
-// A tile of bf16 weights in shared memory, [128 along K][64 rows], 8 elements of padding.
-constexpr int W4_TILE_PITCH = W4_TILE_N + 8;
-
-// rint(x / s) with the correctly rounded quotient; 0 for s = 0.  Out of line: rarely needed.
-__device__ __noinline__ float w4_rounded_quotient(float x, float s) {
-  return s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
-}
-
-// bf16 weights w [E][K][N] (N contiguous) -> packed.  Per group, in fp32, every step one
-// rounding to nearest even: symmetric scale = bf16(max |w| / 7), code = clamp(rint(w / scale)
-// + 8, 0, 15); asymmetric lo = min(w, 0), hi = max(w, 0), scale = bf16((hi - lo) / 15), zero =
-// clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15).  A zero scale
-// gives codes and zero points of 8.  Bound by its bytes (2.5 to 2.6 per weight), so the tile comes
-// and goes in 16-byte vectors, and the division is a multiplication by the reciprocal: that is
-// within 2^-21 of the quotient (at most 16), so only where it lies closer than 2^-16 to the middle
-// between two integers can the rounded quotient be another one, and there it is divided.
-template <bool ZP>
-__global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K,
-                                                          int N, int group,
-                                                          uint8_t* __restrict__ packed) {
-  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
-  __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
-  __shared__ float s_lo[4][W4_TILE_N], s_hi[4][W4_TILE_N];
-  const int R = w4_record(group, ZP), gpb = w4_groups(group);
-  const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
-  const __nv_bfloat16* src = w + ((size_t)e * K + k0) * N + n0;
-#pragma unroll
-  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
-    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
-    if (k0 + k < K && n0 + 8 * v < N)
-      *reinterpret_cast<uint4*>(&tile[k][8 * v]) = __ldg(reinterpret_cast<const uint4*>(src + (size_t)k * N + 8 * v));
-  }
-  __syncthreads();
-  const int row = threadIdx.x & 63, part = threadIdx.x >> 6;   // 32 elements of one row
-  const bool in = n0 + row < N && k0 + 32 * part < K;
-  float v[32];
-  float lo = 0.f, hi = 0.f;
-  if (in) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = __bfloat162float(tile[32 * part + i][row]);
-      lo = fminf(lo, v[i]);
-      hi = fmaxf(hi, v[i]);
-    }
-  }
-  if (group > 32) {
-    s_lo[part][row] = lo;
-    s_hi[part][row] = hi;
-    __syncthreads();
-    const int span = group / 32, p0 = part / span * span;   // the 32-element parts of the group
-    for (int i = p0; i < p0 + span; ++i) {
-      lo = fminf(lo, s_lo[i][row]);
-      hi = fmaxf(hi, s_hi[i][row]);
-    }
-  }
-  if (in) {
-    const __nv_bfloat16 sb = __float2bfloat16_rn(ZP ? __fdiv_rn(__fsub_rn(hi, lo), 15.f)
-                                                    : __fdiv_rn(fmaxf(-lo, hi), 7.f));
-    const float s = __bfloat162float(sb), inv = __fdiv_rn(1.f, s);
-    const bool divide = !(s > 1e-30f && s < 1e30f);   // the reciprocal could leave the normal range
-    const float z = ZP && s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 8.f;
-    const int strip = row >> 4, r = row & 15, block = part >> 1, half = part & 1;
-    uint8_t* b = rec + (strip * 2 + block) * R;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      uint32_t word = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = v[8 * t + j], m = __fmul_rn(x, inv);
-        float q = rintf(m);
-        if (divide || fabsf(fabsf(m - q) - 0.5f) < 0x1p-16f) q = w4_rounded_quotient(x, s);
-        word |= (uint32_t)(int)fminf(fmaxf(q + z, 0.f), 15.f) << (4 * ((j >> 1) + 4 * (j & 1)));
-      }
-      *reinterpret_cast<uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half + 4 * (r >> 3)) = word;
-    }
-    if (half == 0 || gpb == 2) {
-      const int gi = half * (gpb - 1);
-      reinterpret_cast<__nv_bfloat16*>(b + 512)[gi * 16 + w4_row_slot(r)] = sb;
-      if (ZP) b[512 + gpb * 32 + gi * 16 + w4_row_slot(r)] = (uint8_t)z;
-    }
-  }
-  __syncthreads();
-  w4_store_tile(rec, packed, e, n0, k0, K, N, R);
-}
-
-// packed -> bf16 w [E][K][N]: each value rounded once (the difference of the codes is exact, its
-// product with the scale has at most 12 significant bits).  Bound by its bytes, as above.
-__global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __restrict__ packed, int K,
-                                                            int N, int group, int zeros,
-                                                            __nv_bfloat16* __restrict__ w) {
-  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
-  __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
-  const int R = w4_record(group, zeros), gpb = w4_groups(group);
-  const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
-  const int strips = min(4, (N - n0) / W4_ROWS), blocks = min(2, (K - k0) / W4_KB);
-  const int vec = blocks * R / 16;
-  for (int i = threadIdx.x; i < strips * vec; i += 256) {
-    const int s = i / vec, v = i - s * vec;
-    const uint8_t* src =
-        packed + (((size_t)e * (N / W4_ROWS) + n0 / W4_ROWS + s) * (K / W4_KB) + k0 / W4_KB) * R;
-    *reinterpret_cast<uint4*>(rec + s * 2 * R + 16 * v) = __ldg(reinterpret_cast<const uint4*>(src) + v);
-  }
-  __syncthreads();
-  const int row = threadIdx.x & 63, part = threadIdx.x >> 6;
-  if (row < 16 * strips && part < 2 * blocks) {
-    const int r = row & 15, half = part & 1, gi = half * (gpb - 1);
-    const uint8_t* b = rec + ((row >> 4) * 2 + (part >> 1)) * R;
-    const float s = __bfloat162float(
-        reinterpret_cast<const __nv_bfloat16*>(b + 512)[gi * 16 + w4_row_slot(r)]);
-    const float z = zeros ? (float)b[512 + gpb * 32 + gi * 16 + w4_row_slot(r)] : 8.f;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(b + 16 * (4 * (r & 7) + t) + 8 * half +
-                                                               4 * (r >> 3));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        tile[32 * part + 8 * t + j][row] = __float2bfloat16_rn(__fmul_rn((float)w4_nibble(word, j) - z, s));
-    }
-  }
-  __syncthreads();
-  __nv_bfloat16* dst = w + ((size_t)e * K + k0) * N + n0;
-#pragma unroll
-  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
-    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
-    if (k0 + k < K && n0 + 8 * v < N)
-      *reinterpret_cast<uint4*>(dst + (size_t)k * N + 8 * v) = *reinterpret_cast<const uint4*>(&tile[k][8 * v]);
-  }
-}
-
-// ----------------------------------------------------------------------------- the block product
-// D = A B (+ D unless `clear`, a constant) for 16 x 16 A (row-major), 16 x 8 B, bf16 in, fp32 accumulation.  tcgen05.mma would
-// need the decoded weights in shared or tensor memory: a write and a read of four times the
-// bytes that arrive.  Here a lane decodes its 16 bytes in registers, which are already the
-// instruction's operand, and at 16 activation rows the products are far from either rate.
-// (Not volatile: the compiler may interleave independent chains.)
-__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                       uint32_t a3, uint32_t b0, uint32_t b1, bool clear) {
-  const float c0 = clear ? 0.f : d[0], c1 = clear ? 0.f : d[1];
-  const float c2 = clear ? 0.f : d[2], c3 = clear ? 0.f : d[3];
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
 // Decoding.  A pair of codes becomes a pair of exact bf16 values (code - zero) / 4 in one logical
 // operation and one fused multiply-add; the 4 is put back where the sums are joined.  The logical pipe is
 // the scarce one (half the issue rate), so the shifts are kept to one per eight codes:
@@ -286,6 +137,193 @@ __device__ __forceinline__ W4Zero w4_zero(uint32_t zero) {
   z.a = zero * 0x00010001u + 0xC200C200u;                     // -(32 + zero / 4)
   z.b = w4_fma(z.a, 0x3F803F80u /* 1 */, 0x42004200u /* 32 */);
   return z;
+}
+
+// A tile of bf16 weights in shared memory, [128 along K][64 rows], 8 elements of padding.  In the
+// two kernels below a thread has 16 elements along K of two neighbouring rows.
+constexpr int W4_TILE_PITCH = W4_TILE_N + 8;
+__device__ __forceinline__ uint32_t* w4_word(uint8_t* rec, int R, int row, int part, int i) {
+  const int r = row & 15;
+  return reinterpret_cast<uint32_t*>(rec + ((row >> 4) * 2 + (part >> 2)) * R +
+                                     16 * (4 * (r & 7) + 2 * (part & 1) + i) + 8 * ((part >> 1) & 1) +
+                                     4 * (r >> 3));
+}
+
+// rint(x / s) with the correctly rounded quotient; 0 for s = 0.  Out of line: rarely needed.
+__device__ __noinline__ float w4_rounded_quotient(float x, float s) {
+  return s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
+}
+
+// bf16 weights w [E][K][N] (N contiguous) -> packed.  Per group, in fp32, every step one
+// rounding to nearest even: symmetric scale = bf16(max |w| / 7), code = clamp(rint(w / scale)
+// + 8, 0, 15); asymmetric lo = min(w, 0), hi = max(w, 0), scale = bf16((hi - lo) / 15), zero =
+// clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15).  A zero scale
+// gives codes and zero points of 8.
+//
+// Bound by its bytes (2.5 to 2.6 per weight) once the arithmetic is short: the tile comes and
+// goes in 16-byte vectors; the division is a multiplication by the reciprocal, within 2^-19 of the
+// quotient (at most 16); adding 1.5 * 2^23 rounds to an integer in the low bits, and eight of those
+// add up to a packed word when the constant parts are taken off at the end.  The product rounds
+// like the quotient once it has been rounded to a multiple of 2^-11: a weight a 2^i and a scale
+// b 2^j have 8-bit a and b, so a quotient either is a half-integer h or differs from it by at
+// least 2^(j-2) / (b 2^j) > 2^-10.
+template <bool ZP>
+__global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K,
+                                                          int N, int group,
+                                                          uint8_t* __restrict__ packed) {
+  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
+  __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
+  __shared__ __nv_bfloat162 s_lo[8][32], s_hi[8][32];
+  const int R = w4_record(group, ZP), gpb = w4_groups(group);
+  const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
+  const __nv_bfloat16* src = w + ((size_t)e * K + k0) * N + n0;
+#pragma unroll
+  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
+    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
+    if (k0 + k < K && n0 + 8 * v < N)
+      *reinterpret_cast<uint4*>(&tile[k][8 * v]) = __ldg(reinterpret_cast<const uint4*>(src + (size_t)k * N + 8 * v));
+  }
+  __syncthreads();
+  const int pair = threadIdx.x & 31, part = threadIdx.x >> 5;   // rows 2 pair, + 1; k 16 part .. + 15
+  const bool in = n0 + 2 * pair < N && k0 + 16 * part < K;
+  __nv_bfloat162 v[16];
+  __nv_bfloat162 lo = __float2bfloat162_rn(0.f), hi = lo;
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[i] = *reinterpret_cast<const __nv_bfloat162*>(&tile[16 * part + i][2 * pair]);
+      lo = __hmin2(lo, v[i]);
+      hi = __hmax2(hi, v[i]);
+    }
+  }
+  s_lo[part][pair] = lo;
+  s_hi[part][pair] = hi;
+  __syncthreads();
+  if (in) {
+    const int span = group / 16, p0 = part / span * span;   // the 16-element parts of the group
+    for (int i = p0; i < p0 + span; ++i) {
+      lo = __hmin2(lo, s_lo[i][pair]);
+      hi = __hmax2(hi, s_hi[i][pair]);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 2 * pair + c;
+      const float l = c ? __high2float(lo) : __low2float(lo), h = c ? __high2float(hi) : __low2float(hi);
+      const __nv_bfloat16 sb = __float2bfloat16_rn(ZP ? __fdiv_rn(__fsub_rn(h, l), 15.f)
+                                                      : __fdiv_rn(fmaxf(-l, h), 7.f));
+      const float s = __bfloat162float(sb), inv = __fdiv_rn(1.f, s);
+      const int z = ZP && s > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(-l, s)), 0.f), 15.f) : 8;
+      constexpr float ROUND = 12582912.f;             // 1.5 * 2^23
+      constexpr uint32_t BITS = 0x4B400000u;          // its bits
+      constexpr float SNAP = 6144.f;                  // 1.5 * 2^12
+      uint32_t word[2] = {((uint32_t)z - BITS) * 0x11111111u, ((uint32_t)z - BITS) * 0x11111111u};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float x = c ? __high2float(v[i]) : __low2float(v[i]);
+        const float m = __fsub_rn(__fadd_rn(__fmul_rn(x, inv), SNAP), SNAP);
+        uint32_t bits = __float_as_uint(__fadd_rn(m, ROUND));
+        // the rounding of the scale can leave the largest quotient at 16 - zero
+        if (ZP) bits = min(bits, BITS + 15u - (uint32_t)z);
+        word[i >> 3] += bits << (4 * (((i & 7) >> 1) + 4 * (i & 1)));
+      }
+      if (!(s > 1e-30f && s < 1e30f)) {   // the reciprocal or a subnormal: by division
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          uint32_t exact = 0;
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const float x = __bfloat162float(tile[16 * part + 8 * u + i][row]);
+            const float q = w4_rounded_quotient(x, s) + (float)z;
+            exact |= (uint32_t)(int)fminf(fmaxf(q, 0.f), 15.f) << (4 * ((i >> 1) + 4 * (i & 1)));
+          }
+          if (u) word[1] = exact;
+          else word[0] = exact;
+        }
+      }
+      *w4_word(rec, R, row, part, 0) = word[0];
+      *w4_word(rec, R, row, part, 1) = word[1];
+      if ((part & (gpb == 2 ? 1 : 3)) == 0) {
+        uint8_t* b = rec + ((row >> 4) * 2 + (part >> 2)) * R;
+        const int at = ((part >> 1) & (gpb - 1)) * 16 + w4_row_slot(row & 15);
+        reinterpret_cast<__nv_bfloat16*>(b + 512)[at] = sb;
+        if (ZP) b[512 + gpb * 32 + at] = (uint8_t)z;
+      }
+    }
+  }
+  __syncthreads();
+  w4_store_tile(rec, packed, e, n0, k0, K, N, R);
+}
+
+// packed -> bf16 w [E][K][N]: each value rounded once.  Bound by its bytes: codes are decoded in
+// pairs as the products do (a quarter of the difference, exact), times 4, times the scale.
+__global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __restrict__ packed, int K,
+                                                            int N, int group, int zeros,
+                                                            __nv_bfloat16* __restrict__ w) {
+  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
+  __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
+  const int R = w4_record(group, zeros), gpb = w4_groups(group);
+  const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
+  const int strips = min(4, (N - n0) / W4_ROWS), blocks = min(2, (K - k0) / W4_KB);
+  const int vec = blocks * R / 16;
+  for (int i = threadIdx.x; i < strips * vec; i += 256) {
+    const int s = i / vec, v = i - s * vec;
+    const uint8_t* src =
+        packed + (((size_t)e * (N / W4_ROWS) + n0 / W4_ROWS + s) * (K / W4_KB) + k0 / W4_KB) * R;
+    *reinterpret_cast<uint4*>(rec + s * 2 * R + 16 * v) = __ldg(reinterpret_cast<const uint4*>(src) + v);
+  }
+  __syncthreads();
+  const int pair = threadIdx.x & 31, part = threadIdx.x >> 5;
+  if (2 * pair < 16 * strips && part < 4 * blocks) {
+    uint32_t val[2][8];   // per row, pairs along K
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 2 * pair + c;
+      const uint8_t* b = rec + ((row >> 4) * 2 + (part >> 2)) * R;
+      const int at = ((part >> 1) & (gpb - 1)) * 16 + w4_row_slot(row & 15);
+      const uint32_t s2 = reinterpret_cast<const uint16_t*>(b + 512)[at] * 0x00010001u;
+      const W4Zero z = w4_zero(zeros ? b[512 + gpb * 32 + at] : 8u);
+      const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2), four = __float2bfloat162_rn(4.f);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t word = *w4_word(rec, R, row, part, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t d = i & 1 ? w4_high(word >> (4 * (i - 1)), z) : w4_low(word >> (4 * i), z);
+          const __nv_bfloat162 q = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&d), four), s);
+          val[c][4 * u + i] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      *reinterpret_cast<uint32_t*>(&tile[16 * part + 2 * i][2 * pair]) = __byte_perm(val[0][i], val[1][i], 0x5410);
+      *reinterpret_cast<uint32_t*>(&tile[16 * part + 2 * i + 1][2 * pair]) = __byte_perm(val[0][i], val[1][i], 0x7632);
+    }
+  }
+  __syncthreads();
+  __nv_bfloat16* dst = w + ((size_t)e * K + k0) * N + n0;
+#pragma unroll
+  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
+    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
+    if (k0 + k < K && n0 + 8 * v < N)
+      *reinterpret_cast<uint4*>(dst + (size_t)k * N + 8 * v) = *reinterpret_cast<const uint4*>(&tile[k][8 * v]);
+  }
+}
+
+// ----------------------------------------------------------------------------- the block product
+// D = A B (+ D unless `clear`, a constant) for 16 x 16 A (row-major), 16 x 8 B, bf16 in, fp32 accumulation.  tcgen05.mma would
+// need the decoded weights in shared or tensor memory: a write and a read of four times the
+// bytes that arrive.  Here a lane decodes its 16 bytes in registers, which are already the
+// instruction's operand, and at 16 activation rows the products are far from either rate.
+// (Not volatile: the compiler may interleave independent chains.)
+__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1, bool clear) {
+  const float c0 = clear ? 0.f : d[0], c1 = clear ? 0.f : d[1];
+  const float c2 = clear ? 0.f : d[2], c3 = clear ? 0.f : d[3];
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // Reads at a 32-bit shared-memory address (the compiler sees the address space, so offsets fold
