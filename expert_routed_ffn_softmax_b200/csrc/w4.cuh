@@ -326,15 +326,16 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Reads at a 32-bit shared-memory address (the compiler sees the address space, so offsets fold
-// into the load).
+// Reads at a byte offset into the kernel's dynamic shared memory (named, so that the compiler knows
+// the address space and folds constant offsets into the load).
+extern __shared__ __align__(128) uint8_t w4sm[];
 template <typename V>
-__device__ __forceinline__ V lds(uint32_t at) {
-  return *reinterpret_cast<const V*>(__cvta_shared_to_generic(at));
+__device__ __forceinline__ V lds(uint32_t off) {
+  return *reinterpret_cast<const V*>(w4sm + off);
 }
 
 // acc[i][j] += block i * activation fragments, for the records of NS strips at the same place
-// along K, in shared memory: rec[i] = the record's address + 16 lane.  x[j]: the address of the
+// along K, in shared memory: rec[i] = the record's offset + 16 lane.  x[j]: the offset of the
 // lane's 8 activations of the first half (elements 8 t .. + 7 of row g + 8 j, for lane 4 g + t);
 // those of the second half are x_half bytes on.
 // acc[i][j]: (row g, activation rows 8 j + 2 t and + 1), (row g + 8, the same).  The products of

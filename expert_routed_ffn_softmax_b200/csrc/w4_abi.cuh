@@ -30,47 +30,62 @@ auto w4_by_form(int T, int group, bool zeros, F&& fn) {
 // CTAs of the streaming kernels that run at once.
 int w4_slots(const DeviceState& d) { return 2 * std::max(1, d.num_sms); }
 
-// How a linear layer (or the gate | up half of a GEGLU MLP) is cut.  A CTA keeps the activations
-// in shared memory for all of its units where they fit beside a ring of 3 x 16 KB (T K <= 22 K
-// elements, say); longer ones come as fragments with each chunk of weights, so a taller unit reads
-// them less often, while a lower one deals out more evenly.  The cost of a choice is the time of
-// its fullest SM, in bytes at the memory's rate: its units' weights and activations, or the copies
-// that bring them (one is issued in about 0.1 us), and what a unit costs apart from that.
+// How a linear layer (or the gate | up half of a GEGLU MLP) is cut: units of 2 << lg strips,
+// `cluster` CTAs sharing a unit's K.  A CTA keeps its slice of the activations in shared memory
+// where they fit beside the ring (rows up to T K = 22 K elements, say); longer ones come as
+// fragments with each chunk of weights.  A taller unit reads the activations less often, a lower one
+// and slices of K spread a small matrix over the SMs (two CTAs each).  More units than run at once
+// are only stolen without clusters: a cluster's start and meeting would be paid for every unit.
+//
+// The choice is the one with the least time by a model of what was measured on B200 (ns).  Per
+// block and strip, the largest of: decoding and products, 26 with two CTAs on an SM and 18 + 1.1 T
+// with one (45 for two row tiles); its bytes at 22 a ns (32 for a CTA alone on its SM, without
+// fragments); its copies at 100 each.  Per cluster 400 a CTA (200 with fragments, whose own launch
+// hides its start) and 0.3 for every sum exchanged.  Over 17 shapes (T 1 to 16, K 704 to 16384, N
+// 704 to 131072) and all 16 cuts of each, timed one by one, the choice was within 15 % of the best.
 struct W4Plan {
-  int lg = 0, units = 0, step = 0, stage = 0, smem = 0, frag = 0;
+  int lg = 0, cluster = 1, units = 0, step = 0, stage = 0, smem = 0, frag = 0;
 };
 // Whether activations [T][K] come as fragments.
 template <int NB> bool w4_frag(int T, int K) {
-  return NB == 2 || w4_linear_smem<NB>(T, K, 0, 16384).total > W4S_SMEM;
+  return NB == 2 || w4_linear_smem<NB>(T, K, 0, 16384, 1, 0).total > W4S_SMEM;
 }
 template <int NB>
 W4Plan w4_plan(int mode, int T, int K, int N, int record, int sms) {
   W4Plan best;
   best.frag = w4_frag<NB>(T, K);
-  const int kb = K / W4_KB, rest = w4_linear_smem<NB>(T, K, best.frag, 0).total;
-  const int room = std::min((W4S_SMEM - rest) / W4S_STAGES / 128 * 128, 30720);
+  const int kb = K / W4_KB;
   double least = 0;
-  for (int lg = 0; lg < 4; ++lg) {
-    const int strips = 2 << lg, per = mode == W4_GEGLU ? 1 << lg : strips;
-    const int block = strips * record + (best.frag ? w4_frag_block<NB>() : 0);
-    if (room < block) break;
-    W4Plan p = best;
-    p.lg = lg;
-    p.units = (N / W4_ROWS + per - 1) / per;
-    const int chunks = (kb + room / block - 1) / (room / block);
-    p.step = (kb + chunks - 1) / chunks;
-    p.stage = (p.step * block + 127) / 128 * 128;
-    p.smem = w4_linear_smem<NB>(T, K, p.frag, p.stage).total;
-    const int beside = p.units <= sms ? 1 : 2;   // CTAs of an SM
-    const double unit = std::max((double)kb * block, 2400.0 * chunks * (strips + p.frag)) + 8192;
-    // units an SM's CTAs run one after the other; stolen units even out the last round
-    const double rounds = p.units <= 2 * sms ? 1.0 : (double)p.units / (2 * sms) + 0.5;
-    const double cost = beside * rounds * unit;
-    if (least == 0 || cost < least) {
-      least = cost;
-      best = p;
+  for (int cluster = 1; cluster <= 8 && cluster <= kb; cluster *= 2)
+    for (int lg = 0; lg < 4; ++lg) {
+      const int strips = 2 << lg, per = mode == W4_GEGLU ? 1 << lg : strips, most = (kb + cluster - 1) / cluster;
+      const int rest = w4_linear_smem<NB>(T, K, best.frag, 0, cluster, lg).total;
+      const int room = std::min((W4S_SMEM - rest) / W4S_STAGES / 128 * 128, 30720);
+      const int block = strips * record + (best.frag ? w4_frag_block<NB>() : 0);
+      if (room < block) continue;
+      W4Plan p = best;
+      p.lg = lg;
+      p.cluster = cluster;
+      p.units = (N / W4_ROWS + per - 1) / per;
+      const int chunks = (most + room / block - 1) / (room / block);
+      p.step = (most + chunks - 1) / chunks;
+      p.stage = (p.step * block + 127) / 128 * 128;
+      p.smem = w4_linear_smem<NB>(T, K, p.frag, p.stage, cluster, lg).total;
+      const int ctas = p.units * cluster;
+      if (cluster > 1 && ctas > 2 * sms) continue;
+      const double products = NB == 2 ? 45.0 : ctas > sms ? 26.0 : 18.0 + 1.1 * T;
+      const double unit = (double)strips * most *
+                          std::max({products, (double)block / strips / (ctas > sms || p.frag ? 22.0 : 32.0),
+                                    100.0 * (strips + p.frag) / (strips * p.step)});
+      const double act = p.frag ? 0.0 : 128.0 * T * most / 22.0;
+      const double cost = ctas <= 2 * sms
+                              ? unit + act + (cluster > 1 ? (p.frag ? 200.0 : 400.0) * cluster + 0.3 * (32 << lg) * T : 0.0)
+                              : (p.units / (2.0 * sms) + 1.0) * (unit + 250.0) + act;
+      if (least == 0 || cost < least) {
+        least = cost;
+        best = p;
+      }
     }
-  }
   return best;
 }
 
@@ -81,14 +96,28 @@ moe_status_t w4_stream(cudaStream_t st, const DeviceState& d, W4Linear a, int gr
     const int sms = std::max(1, d.num_sms);
     const W4Plan p = w4_plan<NB>(MODE, a.T, a.K, a.N, w4_record(group, zeros), sms);
     a.lg = p.lg;
+    a.cluster = p.cluster;
     a.units = p.units;
     a.step = p.step;
     a.stage = p.stage;
     a.frag = p.frag;
-    a.steal = p.units > 2 * sms;
-    const Launch launch{st, true};
-    launch(true, w4_linear_kernel<NB, decltype(g32)::value, decltype(zp)::value, MODE>, dim3(p.units),
-           dim3(W4S_THREADS), p.smem, a);
+    a.steal = p.cluster == 1 && p.units > 2 * sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.units * p.cluster);
+    cfg.blockDim = dim3(W4S_THREADS);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    cudaLaunchKernelEx(&cfg, w4_linear_kernel<NB, decltype(g32)::value, decltype(zp)::value, MODE>, a);
+    ++t_kernels;
   });
   return launched();
 }
@@ -155,7 +184,8 @@ DeviceState* w4_device_state(int* dev) {
 // the weighted expert outputs.
 struct W4Layout {
   size_t logit = 0, xn2 = 0, wn2 = 0, stats = 0, ids = 0, wts = 0, ctr = 0, h = 0, o = 0, total = 0;
-  int slices = 0, lg2 = 0, n_ctr = 0;
+  size_t xfrag = 0, hfrag = 0;
+  int slices = 0, n_ctr = 0;
 };
 W4Layout w4_layout(int T, int H, int E, int I, int k) {
   W4Layout L;
@@ -167,8 +197,6 @@ W4Layout w4_layout(int T, int H, int E, int I, int k) {
   };
   const size_t P = (size_t)T * k;
   L.slices = H / W4M_SLICE;
-  // W_down units of 64 rows: at the layer's I = 704 their four copies are a chunk of 24 KB
-  L.lg2 = 1;
   L.n_ctr = W4M_CTR_O + H / W4_ROWS;
   L.logit = take(sizeof(double) * L.slices * T * E);
   L.xn2 = take(sizeof(double) * L.slices * T);
@@ -179,6 +207,10 @@ W4Layout w4_layout(int T, int H, int E, int I, int k) {
   L.ctr = take(sizeof(int) * L.n_ctr);
   L.h = take(2 * P * I);
   L.o = take(sizeof(float) * P * H);
+  // fragments of x, and of h per expert with many rows (fewer than P / 3 of them)
+  const size_t block = T > 8 ? w4_frag_block<2>() : w4_frag_block<1>();
+  L.xfrag = take(block * (H / W4_KB));
+  L.hfrag = take(block * (I / W4_KB) * std::min<size_t>(E, P));
   L.total = at;
   return L;
 }
@@ -374,7 +406,6 @@ moe_status_t moe_forward_w4(const void* x, const void* w_router, const float* ro
   a.I = I;
   a.k = k;
   a.renorm = (flags & MOE_FLAG_NO_RENORM) ? 0 : 1;
-  a.lg2 = W.lg2;
   const double u = std::ldexp(1.0, -53), n = (double)H + 8.0;
   a.beta_scale = 2.0 * (n * u / (1.0 - n * u)) * 1.01;
   a.ids = (aux && aux->topk_ids) ? aux->topk_ids : reinterpret_cast<int32_t*>(ws + W.ids);
@@ -386,10 +417,12 @@ moe_status_t moe_forward_w4(const void* x, const void* w_router, const float* ro
   a.ctr = reinterpret_cast<int*>(ws + W.ctr);
   a.h = reinterpret_cast<__nv_bfloat16*>(ws + W.h);
   a.o = reinterpret_cast<float*>(ws + W.o);
+  a.xfrag = reinterpret_cast<__nv_bfloat16*>(ws + W.xfrag);
+  a.hfrag = reinterpret_cast<__nv_bfloat16*>(ws + W.hfrag);
   a.y = static_cast<__nv_bfloat16*>(y);
   const Launch launch{static_cast<cudaStream_t>(stream), true};
   launch(true, w4_front_kernel, dim3(W.slices, (T + W4M_TT - 1) / W4M_TT), dim3(W4M_FRONT_THREADS), 0, a.x,
-         a.wr, T, H, E, logit, xn2, wn2, a.ctr, W.n_ctr, a.stats, a.ids, k);
+         a.wr, T, H, E, logit, xn2, wn2, a.ctr, W.n_ctr, a.stats, a.ids, k, a.xfrag);
   if (const moe_status_t s = launched(); s != MOE_OK) return s;
   w4_by_form(T, group, flags & MOE_FLAG_W4_ZEROS, [&](auto nb, auto g32, auto zp) {
     constexpr int NB = decltype(nb)::value;

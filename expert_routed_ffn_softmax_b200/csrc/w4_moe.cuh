@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(W4M_FRONT_THREADS) w4_front_kernel(
     const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wr, int T, int H, int E,
     double* __restrict__ part_logit, double* __restrict__ part_xn2, double* __restrict__ part_wn2,
     int* __restrict__ counters, int n_counters, unsigned* __restrict__ stats, int32_t* __restrict__ ids,
-    int k) {
+    int k, __nv_bfloat16* __restrict__ xfrag) {
   constexpr int TT = W4M_TT;
   pdl_wait();
   pdl_trigger();
@@ -66,7 +66,9 @@ __global__ void __launch_bounds__(W4M_FRONT_THREADS) w4_front_kernel(
   load(0);
   {
     const int t = tid / W4M_SLICE, h = tid % W4M_SLICE;   // 4 tokens x 64 rows = one element a thread
-    xs[h][t] = t < nt ? (double)__bfloat162float(x[(size_t)(t0 + t) * H + h0 + h]) : 0.0;
+    const __nv_bfloat16 v = t < nt ? x[(size_t)(t0 + t) * H + h0 + h] : __float2bfloat16_rn(0.f);
+    xs[h][t] = (double)__bfloat162float(v);
+    if (t < nt) xfrag[w4_frag_index(T > 8 ? 2 : 1, t0 + t, h0 + h)] = v;
   }
   __syncthreads();
   double acc[TT][2], wn[2] = {0.0, 0.0};
@@ -131,7 +133,7 @@ struct W4Moe {
   const uint8_t *wg, *wu, *wd;      // packed experts
   const double *part_logit, *part_xn2, *part_wn2;
   int slices;                       // of the front kernel
-  int T, H, E, I, k, renorm, lg2;   // lg2: log2 of the row groups of a W_down unit
+  int T, H, E, I, k, renorm;
   double beta_scale;
   int32_t* ids;
   float* wts;
@@ -142,6 +144,9 @@ struct W4Moe {
   // h_ready [128] per active expert, o_ready [row blocks of W_down]
   int* ctr;
   __nv_bfloat16* h;                 // [T k][I]
+  // activations of experts with many rows: x of all tokens, h per active expert, as fragments with
+  // a column per token
+  __nv_bfloat16 *xfrag, *hfrag;
   float* o;                         // [T k][H]: expert outputs
   __nv_bfloat16* y;
 };
@@ -295,10 +300,13 @@ struct W4List {
   int* expert;  // [128] ids of the active experts
   int* info;    // {active experts}
 };
+// An expert of more rows than this takes its activations as fragments of all tokens (one copy a
+// chunk, columns of other tokens unused); fewer rows are copied one by one.
+constexpr int W4M_NARROW = 3;
 
 // sIds: the ids of all pairs (past T k: larger than any), then 8 ints of scratch; 16-byte aligned.
 __device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, int* sIds, int stage,
-                                                int record) {
+                                                int record, int frag_block, int& lg1, int& lg2) {
   const int tid = threadIdx.x, P = a.T * a.k;
   unsigned* sMask = reinterpret_cast<unsigned*>(sIds + W4M_MAX_PAIRS);   // active experts, one bit each
   const int id = tid < W4M_MAX_PAIRS ? sIds[tid] : 0x7fffffff;
@@ -337,14 +345,22 @@ __device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, 
     *L.info = n;
   }
   __syncthreads();
+  // Strips of a unit: 2 << lg1 (gate and up of 16 << lg1 features) and 2 << lg2.  Where experts hold
+  // many rows a taller unit reads the activations less often; it takes enough units, though, to go
+  // round.
+  const bool many = P > W4M_NARROW * n;
+  lg1 = many && n * (a.I / W4_ROWS) / 2 >= (int)gridDim.x ? 1 : 0;
+  lg2 = many && n * (a.H / W4_ROWS) / 8 >= (int)gridDim.x ? 2 : 1;
   if (tid < n) {
     // blocks per chunk: as many as fit a stage, evened out over the unit
     const int rows = L.off[tid + 1] - L.off[tid];
     auto even = [&](int kb, int strips) {
-      const int most = (stage - 64 * rows) / (strips * record + 128 * rows), chunks = (kb + most - 1) / most;
+      const int most = rows > W4M_NARROW ? stage / (strips * record + frag_block)
+                                         : (stage - 64 * rows) / (strips * record + 128 * rows);
+      const int chunks = (kb + most - 1) / most;
       return (kb + chunks - 1) / chunks;
     };
-    L.step[tid] = even(a.H / W4_KB, 2) | even(a.I / W4_KB, 2 << a.lg2) << 16;
+    L.step[tid] = even(a.H / W4_KB, 2 << lg1) | even(a.I / W4_KB, 2 << lg2) << 16;
   }
   __syncthreads();
 }
@@ -372,7 +388,8 @@ struct __align__(16) W4Desc {
   int strips, rows, lg;
   int blocks;   // along K
   int step;     // blocks per chunk
-  int pad[2];
+  int wide;     // 1: activations are fragments
+  int pad;
 };
 constexpr int W4M_DESCS = W4S_STAGES + 1;
 constexpr int W4M_LISTS = 4 * (4 + 4 * W4M_MAX_PAIRS + 4);
@@ -384,8 +401,7 @@ template <int NB> __host__ __device__ constexpr int w4m_stage() {
 template <int NB, bool G32, bool ZP>
 __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_constant__ W4Moe a) {
   constexpr int R = 512 + (G32 ? 2 : 1) * (ZP ? 48 : 32);
-  constexpr int STAGE = w4m_stage<NB>();
-  extern __shared__ __align__(128) uint8_t w4sm[];
+  constexpr int STAGE = w4m_stage<NB>(), FB = w4_frag_block<NB>();
   uint8_t* at = w4sm + W4S_STAGES * STAGE;
   float* acc_tiles = reinterpret_cast<float*>(at);
   at += 2 * w4s_acc_bytes<NB>();
@@ -442,20 +458,22 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
     }
     __syncthreads();
   }
-  w4_build_lists(a, list, sIds, STAGE, R);
+  int lg1, lg2;
+  w4_build_lists(a, list, sIds, STAGE, R, FB, lg1, lg2);
   if (blockIdx.x == 0 && (a.counts || a.offsets || a.perm)) {
     w4_write_aux(a, list, sIds);
     __syncthreads();
   }
   const int n_act = *list.info;
   const int kb1 = a.H / W4_KB, kb2 = a.I / W4_KB, strips1 = a.I / W4_ROWS, strips2 = a.H / W4_ROWS;
-  const int nb2 = (strips2 + (2 << a.lg2) - 1) >> (a.lg2 + 1);   // W_down row blocks
-  const int U1 = n_act * strips1, units = U1 + n_act * nb2;
-  // v / per = umulhi(v, magic) for v * per < 2^32 (at most 128 * 512 * 1024... units)
-  const unsigned magic1 = 0xffffffffu / strips1 + 1, magic2 = 0xffffffffu / nb2 + 1;
+  const int nb1 = strips1 >> lg1;                            // gate | up units of an expert (I % 64 == 0)
+  const int nb2 = (strips2 + (2 << lg2) - 1) >> (lg2 + 1);   // W_down row blocks
+  const int U1 = n_act * nb1, units = U1 + n_act * nb2;
+  // v / per = umulhi(v, magic), exact as v * per < 2^32 (at most 128 * 512 units of 512 an expert)
+  const unsigned magic1 = 0xffffffffu / nb1 + 1, magic2 = 0xffffffffu / nb2 + 1;
   auto split = [&](int c, bool& down, int& ai, int& blk) {
     down = c >= U1;
-    const int v = down ? c - U1 : c, per = down ? nb2 : strips1;
+    const int v = down ? c - U1 : c, per = down ? nb2 : nb1;
     ai = per == 1 ? v : (int)__umulhi((unsigned)v, down ? magic2 : magic1);
     blk = v - ai * per;
   };
@@ -483,31 +501,37 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
         int ai, blk;
         split(c, down, ai, blk);
         const int off = list.off[ai], rows = list.off[ai + 1] - off, e = list.expert[ai];
-        const int lg = down ? a.lg2 : 0, s0 = down ? blk << (lg + 1) : blk, kb = down ? kb2 : kb1;
-        const int strips = down ? min(2 << lg, strips2 - s0) : 2;
+        const bool wide = rows > W4M_NARROW;
+        const int lg = down ? lg2 : lg1, s0 = down ? blk << (lg + 1) : blk << lg, kb = down ? kb2 : kb1;
+        const int strips = down ? min(2 << lg, strips2 - s0) : 2 << lg;
         const size_t pitch = (size_t)kb * R;
         const size_t w_at = ((size_t)e * (down ? strips2 : strips1) + s0) * pitch;
         const int step = down ? list.step[ai] >> 16 : list.step[ai] & 0xffff;
         int4* d = reinterpret_cast<int4*>(descs + n_unit % W4M_DESCS);
         const int width = down ? a.I : a.H;
-        const __nv_bfloat16* act = down ? a.h : a.x;
+        const __nv_bfloat16* act = wide ? (down ? a.hfrag + (size_t)ai * kb2 * (FB / 2) : a.xfrag) : down ? a.h : a.x;
+        const int row_bytes = wide ? FB : 128 * rows;   // activations of a block
         // weights and activation rows of the chunk at block b, into stage s
         auto weights = [&](int b, int s) {
           const uint32_t bytes = min(step, kb - b) * R;
           uint32_t dst = ring + s * STAGE;
-          mbar_arrive_expect_tx(sy.full(s), strips * bytes + rows * 128 * min(step, kb - b));
+          mbar_arrive_expect_tx(sy.full(s), strips * bytes + row_bytes * min(step, kb - b));
           if (down) {
             const uint8_t* src = a.wd + w_at + (size_t)b * R;
             for (int i = 0; i < strips; ++i, src += pitch, dst += bytes) bulk_load(dst, src, bytes, sy.full(s));
           } else {
-            bulk_load(dst, a.wg + w_at + (size_t)b * R, bytes, sy.full(s));
-            bulk_load(dst + bytes, a.wu + w_at + (size_t)b * R, bytes, sy.full(s));
+            size_t from = w_at + (size_t)b * R;
+            for (int i = 0; i < strips; i += 2, from += pitch, dst += 2 * bytes) {
+              bulk_load(dst, a.wg + from, bytes, sy.full(s));
+              bulk_load(dst + bytes, a.wu + from, bytes, sy.full(s));
+            }
           }
         };
         auto activations = [&](int b, int s) {
           const int n = min(step, kb - b);
           uint32_t dst = ring + s * STAGE + strips * n * R;
-          for (int i = 0; i < rows; ++i, dst += 128 * n + 64) {
+          if (wide) bulk_load(dst, act + (size_t)b * (FB / 2), n * FB, sy.full(s));
+          for (int i = 0; !wide && i < rows; ++i, dst += 128 * n + 64) {
             const int pair = list.pair[off + i];
             bulk_load(dst, act + (size_t)(down ? pair : pair / a.k) * width + 64 * b, 128 * n, sy.full(s));
           }
@@ -522,14 +546,14 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
             if (!ok) break;
             if (n == 0) {
               d[0] = make_int4(c, strips, rows, lg);
-              d[1] = make_int4(kb, step, 0, 0);
+              d[1] = make_int4(kb, step, wide, 0);
             }
             weights(n * step, pos.s);
             ++q;
             pos.next();
           }
           if (ok && !all_h) {
-            ok = w4m_wait(h_ready + ai, strips1);
+            ok = w4m_wait(h_ready + ai, nb1);
             all_h = ld_acquire_gpu(a.ctr + 4) == U1;
           }
           fence_proxy_async_global();
@@ -542,7 +566,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
           if (!ok) break;
           if (b == 0) {
             d[0] = make_int4(c, strips, rows, lg);
-            d[1] = make_int4(kb, step, 0, 0);
+            d[1] = make_int4(kb, step, wide, 0);
           }
           weights(b, pos.s);
           activations(b, pos.s);
@@ -572,9 +596,11 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
         ok = false;
         break;
       }
-      const uint32_t head = smem_u32(descs + n_unit % W4M_DESCS);
+      const uint32_t head = (uint32_t)(reinterpret_cast<const uint8_t*>(descs + n_unit % W4M_DESCS) - w4sm);
       const uint4 d0 = lds<uint4>(head), d1 = lds<uint4>(head + 16);
       const int unit = (int)d0.x, strips = d0.y, rows = d0.z, lg = d0.w, kb = d1.x, step = d1.y;
+      const bool wide = d1.z;
+      const uint32_t x_block = wide ? FB : 128, x_half = wide ? NB * 512 : 64;
       const int slices = W4S_MMA_WARPS >> lg, group = warp & ((1 << lg) - 1), slice = warp >> lg;
       for (int b = 0; unit >= 0 && b < kb; b += step) {
         if (b && !w4s_wait(sy.full(pos.s), pos.phase)) {
@@ -587,16 +613,17 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
           const int n = min(step, kb - b);
           // this warp's blocks: those whose place along K is `slice` modulo the slices
           const int f = (slice - b) & (slices - 1);
-          const uint32_t st = smem_u32(w4sm) + pos.s * STAGE;
+          const uint32_t st = pos.s * STAGE;
           // a unit's odd last strip is multiplied twice; the second sum is not read
           const uint32_t to1 = 2 * group + 1 < strips ? n * R : 0;
           uint32_t xr[NB];
 #pragma unroll
           for (int j = 0; j < NB; ++j)
-            xr[j] = st + strips * n * R + min(g + 8 * j, rows - 1) * (128 * n + 64) + 128 * f + 16 * t;
+            xr[j] = st + strips * n * R + f * x_block +
+                    (wide ? 512 * j + 16 * lane : min(g + 8 * j, rows - 1) * (128 * n + 64) + 16 * t);
           w4s_blocks<NB, G32, ZP>(acc, (n - f + slices - 1) >> (3 - lg),
-                                  st + (2 * group * n + f) * R + 16 * lane, to1, slices * R, xr, 128 * slices,
-                                  64, lane);
+                                  st + (2 * group * n + f) * R + 16 * lane, to1, slices * R, xr,
+                                  x_block * slices, x_half, lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.empty(pos.s));
@@ -641,19 +668,26 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
       bool down;
       int ai, blk;
       split(u.x, down, ai, blk);
-      const int off = list.off[ai];
+      const int off = list.off[ai], rows = u.z;
+      const bool wide = rows > W4M_NARROW;
       if (!down) {
-        for (int i = lane; i < 16 * u.z; i += 32) {
-          const int r = i & 15, c = i >> 4;
-          const float gt = w4s_join<NB>(acc, 0, 0, c, r), up = w4s_join<NB>(acc, 0, 1, c, r);
-          a.h[(size_t)list.pair[off + c] * a.I + 16 * blk + r] = __float2bfloat16_rn(w4_geglu(gt, up));
+        const int feats = 16 << lg1;
+        for (int i = lane; i < feats * rows; i += 32) {
+          const int r = i & (feats - 1), c = i >> (lg1 + 4), n = feats * blk + r;
+          const int pair = list.pair[off + c], col = wide ? pair / a.k : c;
+          const float gt = w4s_join<NB>(acc, u.w, 2 * (r >> 4), col, r & 15);
+          const float up = w4s_join<NB>(acc, u.w, 2 * (r >> 4) + 1, col, r & 15);
+          const __nv_bfloat16 h = __float2bfloat16_rn(w4_geglu(gt, up));
+          if (wide) a.hfrag[(size_t)ai * kb2 * (FB / 2) + w4_frag_index(NB, col, n)] = h;
+          else a.h[(size_t)pair * a.I + n] = h;
         }
       } else {
-        const int n0 = (blk << (a.lg2 + 1)) * W4_ROWS;
-        for (int c = 0; c < u.z; ++c) {
-          float* o = a.o + (size_t)list.pair[off + c] * a.H + n0;
+        const int n0 = (blk << (lg2 + 1)) * W4_ROWS;
+        for (int c = 0; c < rows; ++c) {
+          const int pair = list.pair[off + c], col = wide ? pair / a.k : c;
+          float* o = a.o + (size_t)pair * a.H + n0;
 #pragma unroll 2
-          for (int i = lane; i < 16 * u.y; i += 32) o[i] = w4s_join<NB>(acc, u.w, i >> 4, c, i & 15);
+          for (int i = lane; i < 16 * u.y; i += 32) o[i] = w4s_join<NB>(acc, u.w, i >> 4, col, i & 15);
         }
       }
       __syncwarp();
@@ -676,7 +710,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
   const int share = (items + gridDim.x - 1) / gridDim.x;
   for (int i = blockIdx.x * share + tid; i < min(items, (int)(blockIdx.x + 1) * share); i += W4S_THREADS) {
     const int t = i / quads, n = 4 * (i - t * quads);
-    if (!w4m_wait(o_ready + (n / W4_ROWS >> (a.lg2 + 1)), n_act) || !w4m_wait(a.ctr + 3, a.T))
+    if (!w4m_wait(o_ready + (n / W4_ROWS >> (lg2 + 1)), n_act) || !w4m_wait(a.ctr + 3, a.T))
       return;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < a.k; ++j) {

@@ -231,24 +231,28 @@ struct W4Linear {
   int frag;                     // 1: act holds fragments and a chunk brings its blocks' along;
                                 // 0: a CTA keeps all of act in shared memory
   int out_frag;                 // GEGLU: h is written as fragments of this many row tiles (or 0)
-  int steal;                    // 1: more units than CTAs run at once
+  int cluster;                  // CTAs that share a unit's K (1, 2, 4 or 8)
+  int steal;                    // 1: more units than CTAs run at once (cluster 1)
   int early;                    // 1: the previous kernel does not write the weights and started
                                 // after every kernel before it had ended: the first weight
                                 // copies may start before it has ended
 };
 
-// Shared memory: ring, activations (rows 64 bytes apart, so that the two rows a quarter warp reads
-// fall in different halves of the banks), accumulator tiles, ids, barriers.
+// Shared memory: ring, activations of the CTA's slice of K (rows 64 bytes apart, so that the two
+// rows a quarter warp reads fall in different halves of the banks), accumulator tiles, the
+// cluster's partial sums, ids, barriers.
 struct W4LinearSmem {
-  int act, acc, answer, unit, sync, total;
+  int act, acc, part, answer, unit, sync, total;
 };
 constexpr int W4S_UNITS = W4S_STAGES + 1;   // unit ids in flight from the producer to the others
 template <int NB>
-__host__ __device__ inline W4LinearSmem w4_linear_smem(int T, int K, int frag, int stage) {
+__host__ __device__ inline W4LinearSmem w4_linear_smem(int T, int K, int frag, int stage, int cluster, int lg) {
   W4LinearSmem L;
+  const int most = (K / W4_KB + cluster - 1) / cluster;   // blocks of a CTA's slice of K
   L.act = W4S_STAGES * stage;
-  L.acc = L.act + (frag ? 0 : T * (2 * K + 64));
-  L.answer = L.acc + 2 * w4s_acc_bytes<NB>();
+  L.acc = L.act + (frag ? 0 : T * (128 * most + 64));
+  L.part = L.acc + (cluster > 1 ? 1 : 2) * w4s_acc_bytes<NB>();
+  L.answer = (L.part + (cluster > 1 ? (32 << lg) * T * 4 : 0) + 15) / 16 * 16;
   L.unit = L.answer + 16;
   L.sync = L.unit + 4 * (W4S_UNITS + 2 + 2);
   L.total = L.sync + W4Sync::BYTES;
@@ -256,17 +260,20 @@ __host__ __device__ inline W4LinearSmem w4_linear_smem(int T, int K, int frag, i
 }
 
 // Units: 2 << lg strips (GEGLU: the gate and up strips of 16 << lg features, in turn).  A CTA
-// starts with the unit of its block index and takes over units of CTAs that have not started.
+// starts with the unit of its block index and takes over units of CTAs that have not started.  A
+// cluster takes one unit, each CTA a slice of K, and CTA r adds the r-th part of the unit's outputs
+// over the CTAs, in rank order: taller units read the activations less often, and the slices keep
+// every SM busy.
 template <int NB, bool G32, bool ZP, int MODE>
 __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_constant__ W4Linear a) {
   constexpr int R = 512 + (G32 ? 2 : 1) * (ZP ? 48 : 32);
   constexpr int FB = w4_frag_block<NB>();
-  extern __shared__ __align__(128) uint8_t w4sm[];
-  const W4LinearSmem SL = w4_linear_smem<NB>(a.T, a.K, a.frag, a.stage);
+  const W4LinearSmem SL = w4_linear_smem<NB>(a.T, a.K, a.frag, a.stage, a.cluster, a.lg);
   W4Sync sy;
   sy.init(w4sm + SL.sync);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) sy.reset(W4S_EPI_WARPS);
+  if (a.cluster > 1) cluster_sync();   // every CTA of the cluster runs before any stores to it
   if (!a.early) {
     pdl_wait();
     pdl_trigger();
@@ -278,7 +285,10 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
   // has released a later unit's chunk), and on to the joining warps
   int* unit_ring = reinterpret_cast<int*>(w4sm + SL.unit);
   int* acc_unit = unit_ring + W4S_UNITS;
-  const int blocks = a.K / W4_KB, strips_all = a.N / W4_ROWS;
+  const int rank = blockIdx.x % a.cluster, first_unit = blockIdx.x / a.cluster;
+  const int kb = a.K / W4_KB, strips_all = a.N / W4_ROWS;
+  const int k0 = rank * kb / a.cluster, blocks = (rank + 1) * kb / a.cluster - k0;   // slice of K
+  const int act_pitch = 128 * blocks + 64;
   // strips of unit u (its matrix, or of each of gate and up)
   auto strips_of = [&](int u) {
     return MODE == W4_GEGLU ? min(1 << a.lg, strips_all - (u << a.lg))
@@ -287,7 +297,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
   if (warp == W4S_MMA_WARPS + W4S_EPI_WARPS) {
     if (lane == 0) {
       const uint32_t ring = smem_u32(w4sm), answer = smem_u32(w4sm + SL.answer);
-      const size_t pitch = (size_t)blocks * R;
+      const size_t pitch = (size_t)kb * R;
       bool ok = !sy.aborted(), waited = !a.early;
       int q = 0, n_unit = 0, n_steal = 0;
       W4Pos pos;
@@ -297,13 +307,14 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         fence_proxy_async_global();
         if (!a.frag) {
           sy.flags[3] = 1;
-          mbar_arrive_expect_tx(sy.act_full(), a.T * 2 * a.K);
+          mbar_arrive_expect_tx(sy.act_full(), a.T * 128 * blocks);
           for (int t = 0; t < a.T; ++t)
-            bulk_load(smem_u32(w4sm + SL.act) + t * (2 * a.K + 64), a.act + (size_t)t * a.K, 2 * a.K, sy.act_full());
+            bulk_load(smem_u32(w4sm + SL.act) + t * act_pitch, a.act + (size_t)t * a.K + 64 * k0, 128 * blocks,
+                      sy.act_full());
         }
         for (int i = 0; a.frag && i < chunks; ++i) {
-          const int n = min(a.step, blocks - i * a.step), ns = (MODE == W4_GEGLU ? 2 : 1) * strips_of(blockIdx.x);
-          bulk_load(ring + i * a.stage + ns * n * R, a.act + (size_t)i * a.step * (FB / 2), n * FB, sy.full(i));
+          const int n = min(a.step, blocks - i * a.step), ns = (MODE == W4_GEGLU ? 2 : 1) * strips_of(first_unit);
+          bulk_load(ring + i * a.stage + ns * n * R, a.act + (size_t)(k0 + i * a.step) * (FB / 2), n * FB, sy.full(i));
         }
         waited = true;
       };
@@ -313,11 +324,11 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         activations(chunks);
       };
       if (ok && waited) activations(0);
-      for (int u = blockIdx.x; u >= 0 && ok; ++n_unit) {
+      for (int u = first_unit; u >= 0 && ok; ++n_unit) {
         unit_ring[n_unit % W4S_UNITS] = u;
         if (a.steal) steal_request(answer, sy.steal_full());
         const int ns = strips_of(u), all = MODE == W4_GEGLU ? 2 * ns : ns;
-        const size_t at = ((size_t)u << (MODE == W4_GEGLU ? a.lg : a.lg + 1)) * pitch;
+        const size_t at = ((size_t)u << (MODE == W4_GEGLU ? a.lg : a.lg + 1)) * pitch + (size_t)k0 * R;
         for (int b = 0; b < blocks; b += a.step, ++q, pos.next()) {
           // in the first unit weights go ahead until the ring is full
           if (!waited && q == W4S_STAGES) wait_previous(q);
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
           } else {
             for (int i = 0; i < ns; ++i, src += pitch, dst += bytes) bulk_load(dst, src, bytes, bar);
           }
-          if (a.frag && waited) bulk_load(dst, a.act + (size_t)b * (FB / 2), n * FB, bar);
+          if (a.frag && waited) bulk_load(dst, a.act + (size_t)(k0 + b) * (FB / 2), n * FB, bar);
         }
         if (!waited) wait_previous(q);
         u = -1;
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         }
       }
       if (!waited) pdl_wait();
-      if (ok) {
+      if (ok && a.cluster == 1) {
         // the end, through a stage of its own
         if (q >= W4S_STAGES && !w4s_wait(sy.empty(pos.s), pos.phase ^ 1)) ok = false;
         unit_ring[n_unit % W4S_UNITS] = -1;
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < NB; ++j)
       x0[j] = a.frag ? 512 * j + 16 * lane
-                     : smem_u32(w4sm + SL.act) + min((lane >> 2) + 8 * j, a.T - 1) * (2 * a.K + 64) + 16 * (lane & 3);
+                     : SL.act + min((lane >> 2) + 8 * j, a.T - 1) * act_pitch + 16 * (lane & 3);
     for (; ok; ++n_acc) {
       int u = -1, ns = 0;
       for (int b = 0; b < blocks; b += a.step) {
@@ -397,7 +408,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
           const int n = min(a.step, blocks - b);
           // this warp's blocks: those whose place along K is `slice` modulo the slices
           const int f = (slice - b) & (slices - 1);
-          const uint32_t st = smem_u32(w4sm) + pos.s * a.stage;
+          const uint32_t st = pos.s * a.stage;
           // a unit's odd last strip is multiplied twice; the second sum is not read
           const uint32_t to1 = 2 * group + 1 < ns ? n * R : 0;
           uint32_t xr[NB];
@@ -412,6 +423,11 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         pos.next();
       }
       if (!ok) break;
+      if (a.cluster > 1) {
+        // one unit: the whole CTA joins it below
+        w4s_put<NB>(acc, smem_u32(w4sm + SL.acc), ((slice << a.lg) + group) * 2, lane);
+        break;
+      }
       const int buf = n_acc & 1;
       if (n_acc >= 2 && !w4s_wait(sy.acc_empty(buf), ((n_acc >> 1) - 1) & 1)) {
         ok = false;
@@ -429,7 +445,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
   } else {
     const int et = tid - 32 * W4S_MMA_WARPS;
     if (a.early) pdl_wait();   // the outputs may be what the previous kernel still reads
-    for (int n = 0;; ++n) {
+    for (int n = 0; a.cluster == 1; ++n) {
       const int buf = n & 1;
       if (sy.aborted() || !w4s_wait(sy.acc_full(buf), (n >> 1) & 1)) {
         sy.abort();
@@ -460,6 +476,42 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
   }
   __syncthreads();
   if (sy.aborted() && tid == 0) sy.drain();
+  if (a.cluster == 1) return;
+  // ---- a cluster's unit: this CTA's sums over its slice of K go to the CTAs that add them.  Rows of
+  // a GEGLU unit are counted in pairs (gate, up) of the same feature.
+  const int rows = 32 << a.lg, share = rows / a.cluster;
+  float* part = reinterpret_cast<float*>(w4sm + SL.part);
+  if (!sy.aborted()) {
+    const float* acc = reinterpret_cast<const float*>(w4sm + SL.acc);
+    for (int i = tid; i < rows * a.T; i += W4S_THREADS) {
+      const int r = i & (rows - 1), c = i >> (a.lg + 5), owner = r / share;
+      const int strip = MODE == W4_GEGLU ? 2 * (r >> 5) + (r & 1) : r >> 4;
+      const int row = MODE == W4_GEGLU ? (r >> 1) & 15 : r & 15;
+      const uint32_t dst = smem_u32(part + (rank * a.T + c) * share + r - owner * share);
+      st_cluster_u32(mapa_shared(dst, owner), __float_as_uint(w4s_join<NB>(acc, a.lg, strip, c, row)));
+    }
+  }
+  cluster_sync();
+  if (sy.aborted()) return;
+  if (a.early) pdl_wait();   // the outputs may be what the previous kernel still reads
+  const int outs = MODE == W4_GEGLU ? share / 2 : share, wide = 16 * strips_of(first_unit);
+  const int n0 = (MODE == W4_GEGLU ? 16 << a.lg : 32 << a.lg) * first_unit;
+  for (int i = tid; i < outs * a.T; i += W4S_THREADS) {
+    const int r = i % outs, c = i / outs, n = rank * outs + r;
+    if (n >= wide) continue;
+    float v = 0.f, up = 0.f;
+    for (int s = 0; s < a.cluster; ++s) {
+      const float* p = part + (s * a.T + c) * share;
+      v += p[MODE == W4_GEGLU ? 2 * r : r];
+      if (MODE == W4_GEGLU) up += p[2 * r + 1];
+    }
+    const size_t o = (size_t)c * a.N + n0 + n;
+    if (MODE == W4_GEGLU)
+      static_cast<__nv_bfloat16*>(a.out)[a.out_frag ? w4_frag_index(a.out_frag, c, n0 + n) : o] =
+          __float2bfloat16_rn(w4_geglu(v, up));
+    else if (MODE == W4_LINEAR_F32) static_cast<float*>(a.out)[o] = v;
+    else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+  }
 }
 
 }  // namespace moe
