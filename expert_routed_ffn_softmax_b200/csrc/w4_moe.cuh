@@ -394,8 +394,8 @@ struct __align__(16) W4Desc {
 constexpr int W4M_DESCS = W4S_STAGES + 1;
 constexpr int W4M_LISTS = 4 * (4 + 4 * W4M_MAX_PAIRS + 4);
 template <int NB> __host__ __device__ constexpr int w4m_stage() {
-  return (W4S_SMEM - 2 * w4s_acc_bytes<NB>() - W4Sync::BYTES - (int)sizeof(W4Desc) * W4M_DESCS - 32 - W4M_LISTS) / 3 /
-         128 * 128;
+  return (W4S_SMEM - 2 * w4s_acc_bytes<NB>() - W4Sync::BYTES - (int)sizeof(W4Desc) * W4M_DESCS - 32 - W4M_LISTS) /
+         W4S_STAGES / 128 * 128;
 }
 
 template <int NB, bool G32, bool ZP>
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
       bool ok = true, all_h = false;
       // Wait for the next stage; false when the CTA gives up.
       auto acquire = [&] {
-        if (sy.aborted() || (q >= W4S_STAGES && !w4s_wait(sy.empty(pos.s), pos.phase ^ 1))) return false;
+        if (sy.aborted() || (q >= W4S_STAGES && !sy.wait(sy.empty(pos.s), pos.phase ^ 1))) return false;
         sy.flags[1] = q + 1;
         return true;
       };
@@ -589,10 +589,9 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < 2 * NB * 4; ++i) acc[i / (4 * NB)][i / 4 % NB][i % 4] = 0.f;
     W4Pos pos;
-    int q = 0;
     bool ok = true;
     for (int n_unit = 0;; ++n_unit) {
-      if (sy.aborted() || !w4s_wait(sy.full(pos.s), pos.phase)) {
+      if (!sy.wait(sy.full(pos.s), pos.phase)) {
         ok = false;
         break;
       }
@@ -603,12 +602,10 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
       const uint32_t x_block = wide ? FB : 128, x_half = wide ? NB * 512 : 64;
       const int slices = W4S_MMA_WARPS >> lg, group = warp & ((1 << lg) - 1), slice = warp >> lg;
       for (int b = 0; unit >= 0 && b < kb; b += step) {
-        if (b && !w4s_wait(sy.full(pos.s), pos.phase)) {
+        if (b && !sy.wait(sy.full(pos.s), pos.phase)) {
           ok = false;
           break;
         }
-        if (warp == 0 && lane == 0) sy.flags[2] = q + 1;
-        ++q;
         if (2 * group < strips) {
           const int n = min(step, kb - b);
           // this warp's blocks: those whose place along K is `slice` modulo the slices
@@ -632,7 +629,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
       if (!ok) break;
       // hand the unit's partial sums (or the end) to the joining warps
       const int buf = n_unit & 1;
-      if (n_unit >= 2 && !w4s_wait(sy.acc_empty(buf), ((n_unit >> 1) - 1) & 1)) {
+      if (n_unit >= 2 && !sy.wait(sy.acc_empty(buf), ((n_unit >> 1) - 1) & 1)) {
         ok = false;
         break;
       }
@@ -644,7 +641,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
       if (unit < 0) {
         // the end, to the other joining warp too
         const int last = buf ^ 1, m = n_unit + 1;
-        ok = m < 2 || w4s_wait(sy.acc_empty(last), ((m >> 1) - 1) & 1);
+        ok = m < 2 || sy.wait(sy.acc_empty(last), ((m >> 1) - 1) & 1);
         if (!ok) break;
         if (warp == 0 && lane == 0) acc_unit[last] = make_int4(-1, 0, 0, 0);
         __syncwarp();
@@ -659,7 +656,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
     const int buf = warp - W4S_MMA_WARPS;
     const float* acc = acc_tiles + buf * (w4s_acc_bytes<NB>() / 4);
     for (int n = 0;; ++n) {
-      if (sy.aborted() || !w4s_wait(sy.acc_full(buf), n & 1)) {
+      if (sy.aborted() || !sy.wait(sy.acc_full(buf), n & 1)) {
         sy.abort();
         break;
       }

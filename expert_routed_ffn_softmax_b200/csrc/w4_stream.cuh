@@ -40,8 +40,9 @@ template <int NB> __host__ __device__ constexpr int w4s_acc_bytes() { return 16 
 enum W4Mode { W4_LINEAR = 0, W4_LINEAR_F32 = 1, W4_GEGLU = 2 };
 
 // Bounded wait for warps that wait long and often beside warps that compute: the hint lets the
-// hardware park the warp until the phase completes.
-__device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity) {
+// hardware park the warp until the phase completes.  False also when the CTA gives up (*abort); that
+// is looked at only when a wait is long, so the usual one costs a few instructions.
+__device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
   constexpr uint32_t kParkNs = 20000;
   uint64_t t0 = 0;
   while (true) {
@@ -54,6 +55,7 @@ __device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity), "r"(kParkNs)
         : "memory");
     if (ok) return true;
+    if (abort && *abort) return false;
     const uint64_t now = global_timer_ns();
     if (t0 == 0) t0 = now;
     if (now - t0 > *reinterpret_cast<volatile unsigned long long*>(&g_wait_limit_ns)) {
@@ -66,7 +68,7 @@ __device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity) {
 // Barriers and flags of a CTA.
 struct W4Sync {
   uint32_t base;
-  volatile int* flags;   // {abort, chunks issued, chunks consumed, activations issued}
+  volatile int* flags;   // {abort, phases issued (chunks, the end), -, activations issued}
   __device__ uint32_t full(int s) const { return base + 8u * s; }
   __device__ uint32_t empty(int s) const { return base + 8u * (W4S_STAGES + s); }
   __device__ uint32_t acc_full(int b) const { return base + 8u * (2 * W4S_STAGES + b); }
@@ -95,9 +97,11 @@ struct W4Sync {
   }
   __device__ void abort() const { flags[0] = 1; }
   __device__ bool aborted() const { return flags[0] != 0; }
-  // After the roles have ended with an abort: wait for chunks that were issued and not consumed.
+  __device__ bool wait(uint32_t bar, uint32_t parity) const { return w4s_wait(bar, parity, flags); }
+  // After the roles have ended with an abort: wait for the copies of the last chunks (a stage is
+  // issued again only when its chunk has been consumed).
   __device__ void drain() const {
-    for (int q = flags[2]; q < flags[1]; ++q)
+    for (int q = max(0, flags[1] - W4S_STAGES); q < flags[1]; ++q)
       mbar_wait_ns(full(q % W4S_STAGES), (q / W4S_STAGES) & 1, kDrainLimitNs);
     if (flags[3]) mbar_wait_ns(act_full(), 0, kDrainLimitNs);
   }
@@ -254,7 +258,7 @@ __host__ __device__ inline W4LinearSmem w4_linear_smem(int T, int K, int frag, i
   L.part = L.acc + (cluster > 1 ? 1 : 2) * w4s_acc_bytes<NB>();
   L.answer = (L.part + (cluster > 1 ? (32 << lg) * T * 4 : 0) + 15) / 16 * 16;
   L.unit = L.answer + 16;
-  L.sync = L.unit + 4 * (W4S_UNITS + 2 + 2);
+  L.sync = L.unit + (W4S_UNITS + 2 + 3) / 4 * 16;   // barriers: 8-byte aligned
   L.total = L.sync + W4Sync::BYTES;
   return L;
 }
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         }
         for (int i = 0; a.frag && i < chunks; ++i) {
           const int n = min(a.step, blocks - i * a.step), ns = (MODE == W4_GEGLU ? 2 : 1) * strips_of(first_unit);
-          bulk_load(ring + i * a.stage + ns * n * R, a.act + (size_t)(k0 + i * a.step) * (FB / 2), n * FB, sy.full(i));
+          bulk_load(ring + i * a.stage + ns * a.step * R, a.act + (size_t)(k0 + i * a.step) * (FB / 2), n * FB, sy.full(i));
         }
         waited = true;
       };
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         for (int b = 0; b < blocks; b += a.step, ++q, pos.next()) {
           // in the first unit weights go ahead until the ring is full
           if (!waited && q == W4S_STAGES) wait_previous(q);
-          if (sy.aborted() || (q >= W4S_STAGES && !w4s_wait(sy.empty(pos.s), pos.phase ^ 1))) {
+          if (sy.aborted() || (q >= W4S_STAGES && !sy.wait(sy.empty(pos.s), pos.phase ^ 1))) {
             ok = false;
             break;
           }
@@ -344,12 +348,12 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
           mbar_arrive_expect_tx(bar, all * bytes + (a.frag ? n * FB : 0));
           if (MODE == W4_GEGLU) {
             const uint8_t* up = a.w1 + at + (size_t)b * R;
-            for (int i = 0; i < ns; ++i, src += pitch, up += pitch, dst += 2 * bytes) {
+            for (int i = 0; i < ns; ++i, src += pitch, up += pitch, dst += 2 * a.step * R) {
               bulk_load(dst, src, bytes, bar);
-              bulk_load(dst + bytes, up, bytes, bar);
+              bulk_load(dst + a.step * R, up, bytes, bar);
             }
           } else {
-            for (int i = 0; i < ns; ++i, src += pitch, dst += bytes) bulk_load(dst, src, bytes, bar);
+            for (int i = 0; i < ns; ++i, src += pitch, dst += a.step * R) bulk_load(dst, src, bytes, bar);
           }
           if (a.frag && waited) bulk_load(dst, a.act + (size_t)(k0 + b) * (FB / 2), n * FB, bar);
         }
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         u = -1;
         if (a.steal) {
           // also when giving up: the answer must not arrive in a CTA that has ended
-          if (!w4s_wait(sy.steal_full(), n_steal & 1)) ok = false;
+          if (!w4s_wait(sy.steal_full(), n_steal & 1, nullptr)) ok = false;
           else u = steal_answer(answer);
           ++n_steal;
         }
@@ -365,9 +369,12 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
       if (!waited) pdl_wait();
       if (ok && a.cluster == 1) {
         // the end, through a stage of its own
-        if (q >= W4S_STAGES && !w4s_wait(sy.empty(pos.s), pos.phase ^ 1)) ok = false;
+        if (q >= W4S_STAGES && !sy.wait(sy.empty(pos.s), pos.phase ^ 1)) ok = false;
         unit_ring[n_unit % W4S_UNITS] = -1;
-        if (ok) mbar_arrive(sy.full(pos.s));
+        if (ok) {
+          sy.flags[1] = q + 1;
+          mbar_arrive(sy.full(pos.s));
+        }
       }
       if (!ok) sy.abort();
     }
@@ -377,46 +384,49 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 2 * NB * 4; ++i) acc[i / (4 * NB)][i / 4 % NB][i % 4] = 0.f;
     W4Pos pos;
-    int q = 0, n_acc = 0;
+    int n_acc = 0;
     bool ok = true;
-    // this lane's activations: of its rows in shared memory (from block 0), or of a fragment
-    uint32_t x0[NB];
+    // This lane's activations (of its rows in shared memory, from block 0; or of a stage's fragments)
+    // and weights (of a stage); a chunk's strips are a.step blocks apart whatever it holds
     const uint32_t x_half = a.frag ? NB * 512 : 64, x_block = a.frag ? FB : 128;
+    const uint32_t strip = a.step * R, w0 = 2 * group * strip + 16 * lane;
+    uint32_t x0[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
       x0[j] = a.frag ? 512 * j + 16 * lane
                      : SL.act + min((lane >> 2) + 8 * j, a.T - 1) * act_pitch + 16 * (lane & 3);
     for (; ok; ++n_acc) {
-      int u = -1, ns = 0;
+      int u = -1;
+      uint32_t to1 = 0, x_at = 0;
+      bool mine = false;
       for (int b = 0; b < blocks; b += a.step) {
-        if (sy.aborted() || !w4s_wait(sy.full(pos.s), pos.phase)) {
+        if (!sy.wait(sy.full(pos.s), pos.phase)) {
           ok = false;
           break;
         }
         if (b == 0) {
           u = unit_ring[n_acc % W4S_UNITS];
           if (u < 0) break;
-          ns = (MODE == W4_GEGLU ? 2 : 1) * strips_of(u);
-          if (n_acc == 0 && !a.frag && !w4s_wait(sy.act_full(), 0)) {
+          const int ns = (MODE == W4_GEGLU ? 2 : 1) * strips_of(u);
+          mine = 2 * group < ns;
+          // a unit's odd last strip is multiplied twice; the second sum is not read
+          to1 = 2 * group + 1 < ns ? strip : 0;
+          x_at = a.frag ? ns * strip : 0;
+          if (n_acc == 0 && !a.frag && !sy.wait(sy.act_full(), 0)) {
             ok = false;
             break;
           }
         }
-        if (warp == 0 && lane == 0) sy.flags[2] = q + 1;
-        ++q;
-        if (2 * group < ns) {
-          const int n = min(a.step, blocks - b);
+        if (mine) {
           // this warp's blocks: those whose place along K is `slice` modulo the slices
           const int f = (slice - b) & (slices - 1);
-          const uint32_t st = pos.s * a.stage;
-          // a unit's odd last strip is multiplied twice; the second sum is not read
-          const uint32_t to1 = 2 * group + 1 < ns ? n * R : 0;
+          const uint32_t st = pos.s * a.stage, x_st = (a.frag ? st + x_at : b * 128) + f * x_block;
           uint32_t xr[NB];
 #pragma unroll
-          for (int j = 0; j < NB; ++j) xr[j] = x0[j] + (a.frag ? st + ns * n * R + f * x_block : (b + f) * x_block);
-          w4s_blocks<NB, G32, ZP>(acc, (n - f + slices - 1) >> (3 - a.lg),
-                                  st + (2 * group * n + f) * R + 16 * lane, to1, slices * R, xr,
-                                  x_block * slices, x_half, lane);
+          for (int j = 0; j < NB; ++j) xr[j] = x0[j] + x_st;
+          w4s_blocks<NB, G32, ZP>(acc, (min(a.step, blocks - b) - f + slices - 1) >> (3 - a.lg), st + w0 + f * R,
+                                  to1,
+                                  slices * R, xr, x_block * slices, x_half, lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.empty(pos.s));
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         break;
       }
       const int buf = n_acc & 1;
-      if (n_acc >= 2 && !w4s_wait(sy.acc_empty(buf), ((n_acc >> 1) - 1) & 1)) {
+      if (n_acc >= 2 && !sy.wait(sy.acc_empty(buf), ((n_acc >> 1) - 1) & 1)) {
         ok = false;
         break;
       }
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
     if (a.early) pdl_wait();   // the outputs may be what the previous kernel still reads
     for (int n = 0; a.cluster == 1; ++n) {
       const int buf = n & 1;
-      if (sy.aborted() || !w4s_wait(sy.acc_full(buf), (n >> 1) & 1)) {
+      if (sy.aborted() || !sy.wait(sy.acc_full(buf), (n >> 1) & 1)) {
         sy.abort();
         break;
       }
