@@ -553,12 +553,12 @@ def _rows(x, name: str):
     return x.shape
 
 
-def _w4_empty(E: int, K: int, N: int, group: int, zeros: bool, dev) -> W4Weights:
+def _w4_empty(E: int, K: int, N: int, group: int, zeros: bool, like) -> W4Weights:
     n = load().moe_w4_packed_bytes(E, K, N, group, MOE_FLAG_W4_ZEROS if zeros else 0)
     if n == 0:
         raise MoEError(MOE_ERR_UNSUPPORTED if group in (32, 64, 128) else MOE_ERR_INVALID_ARG,
                        "moe_w4_packed_bytes")
-    data = torch.empty((E, N // 16, K // 64, n // (E * (N // 16) * (K // 64))), dtype=_U8, device=dev)
+    data = like.new_empty((E, N // 16, K // 64, n // (E * (N // 16) * (K // 64))), dtype=_U8)
     return W4Weights(data, E, K, N, group, zeros)
 
 
@@ -578,7 +578,7 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | Non
         raise ValueError(f"codes must be [E, N, K/2] or [N, K/2], got {tuple(codes.shape)}")
     E, N, half = codes.shape
     K, dev = 2 * half, codes.get_device()
-    w = _w4_empty(E, K, N, group, zeros is not None, codes.device)
+    w = _w4_empty(E, K, N, group, zeros is not None, codes)
     G = -(-K // group)
     pc = _tensor(codes, "codes", _U8, (E, N, half), dev)
     ps = _tensor(scales, "scales", _BF16, (E, N, G), dev)
@@ -602,7 +602,7 @@ def w4_quantize(w: torch.Tensor, group: int = 64, zeros: bool = False, stream=No
     E, K, N = w.shape
     dev = w.get_device()
     pw = _tensor(w, "w", _BF16, (E, K, N), dev)
-    q = _w4_empty(E, K, N, group, zeros, w.device)
+    q = _w4_empty(E, K, N, group, zeros, w)
     _check(load().moe_w4_quantize_weights(pw, E, K, N, group, q.flags, q.data.data_ptr(),
                                           _raw_stream(dev)), "moe_w4_quantize_weights")
     return q
@@ -615,7 +615,7 @@ def w4_dequantize(w: W4Weights, out: torch.Tensor | None = None, stream=None) ->
         raise TypeError("w must be W4Weights on a CUDA device (w4_pack, w4_quantize)")
     if stream is not None or w.index != _current_device():
         return _elsewhere(w4_dequantize, w, stream, (w, out))
-    o = torch.empty(w.shape, dtype=_BF16, device=w.data.device) if out is None else out
+    o = w.data.new_empty(w.shape, dtype=_BF16) if out is None else out
     po = _tensor(o, "out", _BF16, w.shape, w.index)
     _check(load().moe_w4_dequantize_weights(w.data.data_ptr(), w.E, w.K, w.N, w.group, w.flags, po,
                                             _raw_stream(w.index)), "moe_w4_dequantize_weights")
@@ -629,7 +629,7 @@ def _w4_workspace(nbytes: int, given: torch.Tensor | None, what: str, x) -> tupl
     if nbytes == 0:
         raise MoEError(MOE_ERR_UNSUPPORTED, what)
     if given is None:
-        given = torch.empty(nbytes, dtype=_U8, device=x.device)
+        given = x.new_empty(nbytes // 2)   # x is bf16; the sizes are multiples of 256
         return given.data_ptr(), nbytes, given
     n = given.numel()
     return _tensor(given, "workspace_buf", _U8, (n,), x.get_device()), n, given
@@ -653,7 +653,7 @@ def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, fp
     px = _tensor(x, "x", _BF16, (T, K), dev)
     dt = _F32 if fp32 else _BF16
     if out is None:
-        out = torch.empty((T, N), dtype=dt, device=x.device)
+        out = torch.empty((T, N), dtype=dt, device=x.device) if fp32 else x.new_empty((T, N))
         py = out.data_ptr()
     else:
         py = _tensor(out, "out", dt, (T, N), dev)
@@ -693,7 +693,7 @@ def dense_ffn_w4(x: torch.Tensor, w_gate: W4Weights, w_up: W4Weights, w_down: W4
     _w4_same_form(w_gate, w_up, w_down)
     px = _tensor(x, "x", _BF16, (T, H), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=_BF16, device=x.device)
+        out = x.new_empty((T, H))
         py = out.data_ptr()
     else:
         py = _tensor(out, "out", _BF16, (T, H), dev)
@@ -731,7 +731,7 @@ def forward_w4(x: torch.Tensor, w_router: torch.Tensor, w_gate: W4Weights, w_up:
     pr = _tensor(w_router, "w_router", _BF16, (H, E), dev)
     pb = None if bias is None else _tensor(bias, "bias", _F32, (E,), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=_BF16, device=x.device)
+        out = x.new_empty((T, H))
         py = out.data_ptr()
     else:
         py = _tensor(out, "out", _BF16, (T, H), dev)

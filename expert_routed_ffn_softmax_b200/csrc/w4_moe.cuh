@@ -304,53 +304,53 @@ struct W4List {
 // chunk, columns of other tokens unused); fewer rows are copied one by one.
 constexpr int W4M_NARROW = 3;
 
-// sIds: the ids of all pairs (past T k: larger than any), then 8 ints of scratch; 16-byte aligned.
-__device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, int* sIds, int stage,
+// sKeys: 128 id + pair of all pairs (past T k: larger than any), then 4 ints of scratch; 16-byte
+// aligned.
+__device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, int* sKeys, int stage,
                                                 int record, int frag_block, int& lg1, int& lg2) {
   const int tid = threadIdx.x, P = a.T * a.k;
-  unsigned* sMask = reinterpret_cast<unsigned*>(sIds + W4M_MAX_PAIRS);   // active experts, one bit each
-  const int id = tid < W4M_MAX_PAIRS ? sIds[tid] : 0x7fffffff;
-  if (tid < 8) sMask[tid] = 0;
-  __syncthreads();
-  int before = 0, same = 0;
+  unsigned* sFirst = reinterpret_cast<unsigned*>(sKeys + W4M_MAX_PAIRS);   // an expert's first places
   if (tid < P) {
-    atomicOr(&sMask[id >> 5], 1u << (id & 31));
+    const int mine = sKeys[tid];
+    int before = 0;
 #pragma unroll 4
     for (int q = 0; q < P; q += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(sIds + q);
-      const int v[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool eq = v[i] == id && q + i < tid;
-        same += eq;
-        before += eq || v[i] < id;
-      }
+      const int4 o = *reinterpret_cast<const int4*>(sKeys + q);
+      before += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
     }
     L.pair[before] = tid;
   }
   __syncthreads();
-  int n = 0, at = 0;   // active experts, and those before this one
+  // thread = place in expert order from here
+  const int id = tid < P ? sKeys[L.pair[tid]] >> 7 : -1;
+  const bool first = tid < P && (tid == 0 || sKeys[L.pair[tid - 1]] >> 7 != id);
+  const unsigned firsts = __ballot_sync(0xffffffffu, first);
+  if ((tid & 31) == 0 && tid < W4M_MAX_PAIRS) sFirst[tid >> 5] = firsts;
+  __syncthreads();
+  int n = 0, at = __popc(firsts & ((1u << (tid & 31)) - 1));   // active experts, and those before this one
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned m = sMask[i];
-    n += __popc(m);
-    if (tid < P) at += i < id >> 5 ? __popc(m) : i == id >> 5 ? __popc(m & ((1u << (id & 31)) - 1)) : 0;
+  for (int i = 0; i < W4M_MAX_PAIRS / 32; ++i) {
+    const int m = __popc(sFirst[i]);
+    n += m;
+    at += i < tid >> 5 ? m : 0;
   }
-  if (tid < P && same == 0) {
+  if (first) {
     L.expert[at] = id;
-    L.off[at] = before;
+    L.off[at] = tid;
   }
   if (tid == 0) {
     L.off[n] = P;
     *L.info = n;
   }
   __syncthreads();
-  // Strips of a unit: 2 << lg1 (gate and up of 16 << lg1 features) and 2 << lg2.  Where experts hold
-  // many rows a taller unit reads the activations less often; it takes enough units, though, to go
-  // round.
-  const bool many = P > W4M_NARROW * n;
-  lg1 = many && n * (a.I / W4_ROWS) / 2 >= (int)gridDim.x ? 1 : 0;
-  lg2 = many && n * (a.H / W4_ROWS) / 8 >= (int)gridDim.x ? 2 : 1;
+  // Strips of a unit: 2 << lg1 (gate and up of 16 << lg1 features) and 2 << lg2.  A taller unit reads
+  // the activations less often and is published once, but the last round of units is longer: it is
+  // taken with four rounds or more (two where experts hold many rows).  H = 2816, I = 704: 12 tokens
+  // on 68 experts 98 us with low units, 95 with tall ones; 16 tokens on 19 experts (1.4 rounds of tall
+  // ones) 55 and 66.
+  const int rounds = (P > W4M_NARROW * n ? 2 : 4) * gridDim.x;
+  lg1 = n * (a.I / W4_ROWS) / 2 >= rounds ? 1 : 0;
+  lg2 = n * (a.H / W4_ROWS) / 8 >= rounds ? 2 : 1;
   if (tid < n) {
     // blocks per chunk: as many as fit a stage, evened out over the unit
     const int rows = L.off[tid + 1] - L.off[tid];
@@ -366,13 +366,13 @@ __device__ __forceinline__ void w4_build_lists(const W4Moe& a, const W4List& L, 
 }
 
 // Counts, offsets and permutation for the caller (one CTA writes them).
-__device__ __forceinline__ void w4_write_aux(const W4Moe& a, const W4List& L, const int* sIds) {
+__device__ __forceinline__ void w4_write_aux(const W4Moe& a, const W4List& L, const int* sKeys) {
   const int P = a.T * a.k;
   for (int e = threadIdx.x; e <= a.E; e += W4S_THREADS) {
     int less = 0, equal = 0;
     for (int q = 0; q < P; ++q) {
-      less += sIds[q] < e;
-      equal += sIds[q] == e;
+      less += sKeys[q] >> 7 < e;
+      equal += sKeys[q] >> 7 == e;
     }
     if (a.offsets) a.offsets[e] = less;
     if (a.counts && e < a.E) a.counts[e] = equal;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
   // ---- selection: CTA t selects token t.  Every CTA then polls the ids themselves (-1 until they
   // are there).  The CTAs wait for CTAs that may not have started, if other work holds the SMs: one
   // that has waited long takes any token that nobody has claimed, so the wait ends.
-  int* sIds = reinterpret_cast<int*>(acc_tiles);   // scratch until the first unit is joined
+  int* sKeys = reinterpret_cast<int*>(acc_tiles);   // scratch until the first unit is joined
   const int P = a.T * a.k;
   if (tid == 0) {
     const bool dead = *reinterpret_cast<volatile unsigned*>(&g_error_word) & MOE_DEVERR_TIMEOUT;
@@ -440,11 +440,11 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
     if (t < 0) return;   // an earlier launch's wait ran out, or this one's: nothing is in flight
     if (t < a.T) w4_select(a, t, w4sm);
     // wait a while for the ids
-    int id = tid < P ? -1 : 0x7fffffff;
+    int id = tid < P ? -1 : 0xffffff;
     const uint64_t t0 = global_timer_ns();
     while (id < 0 && global_timer_ns() - t0 < 20000)
       id = *reinterpret_cast<const volatile int32_t*>(a.ids + tid);
-    if (tid < W4M_MAX_PAIRS) sIds[tid] = id;
+    if (tid < W4M_MAX_PAIRS) sKeys[tid] = max(id, 0) << 7 | tid;
     if (__syncthreads_and(id >= 0)) break;
     if (tid == 0) {
       int next = a.T;
@@ -459,9 +459,9 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
     __syncthreads();
   }
   int lg1, lg2;
-  w4_build_lists(a, list, sIds, STAGE, R, FB, lg1, lg2);
+  w4_build_lists(a, list, sKeys, STAGE, R, FB, lg1, lg2);
   if (blockIdx.x == 0 && (a.counts || a.offsets || a.perm)) {
-    w4_write_aux(a, list, sIds);
+    w4_write_aux(a, list, sKeys);
     __syncthreads();
   }
   const int n_act = *list.info;
