@@ -58,19 +58,29 @@ __device__ __forceinline__ int w4_row_slot(int r) { return 2 * (r & 7) + (r >> 3
 // A tile of the packing kernels: 64 rows x 128 elements (4 strips x 2 blocks; ragged at the
 // matrix's ends), assembled in shared memory and written as runs of two records per strip.
 constexpr int W4_TILE_N = 64, W4_TILE_K = 128;
-constexpr int W4_TILE_BYTES = 4 * 2 * 608;
+// Bytes between a tile's records: an odd number of 16s, so that strips fall in different banks (a
+// warp's stores of codes met 16 deep at 576 bytes: the quantiser took 193 us instead of 169 for 128
+// matrices of 2816 x 704).
+__host__ __device__ constexpr int w4_tile_pitch(int record) { return record | 16; }
+constexpr int W4_TILE_BYTES = 4 * 2 * w4_tile_pitch(608);
 
-// Write the assembled records [strip][block][R] of tile (n0, k0) of matrix `e`.
+// A record of tile (n0, k0) of matrix `e` for each of 8 warps: strip warp / 2, block warp % 2 (false
+// past the matrix's ends); `at` is its offset in the packed matrices, `in_tile` its offset in the tile.
+__device__ __forceinline__ bool w4_tile_record(int e, int n0, int k0, int K, int N, int R, size_t& at,
+                                               int& in_tile) {
+  const int warp = threadIdx.x >> 5, strip = n0 / W4_ROWS + (warp >> 1), block = k0 / W4_KB + (warp & 1);
+  at = (((size_t)e * (N / W4_ROWS) + strip) * (K / W4_KB) + block) * R;
+  in_tile = warp * w4_tile_pitch(R);
+  return strip < N / W4_ROWS && block < K / W4_KB;
+}
+// Write the assembled records [strip][block][R].
 __device__ __forceinline__ void w4_store_tile(const uint8_t* rec, uint8_t* packed, int e, int n0,
                                               int k0, int K, int N, int R) {
-  const int strips = min(4, (N - n0) / W4_ROWS), blocks = min(2, (K - k0) / W4_KB);
-  const int vec = blocks * R / 16;   // 16-byte vectors per strip: contiguous in both places
-  const size_t kb = K / W4_KB;
-  for (int i = threadIdx.x; i < strips * vec; i += blockDim.x) {
-    const int s = i / vec, v = i - s * vec;
-    uint8_t* dst = packed + (((size_t)e * (N / W4_ROWS) + n0 / W4_ROWS + s) * kb + k0 / W4_KB) * R;
-    reinterpret_cast<uint4*>(dst)[v] = *reinterpret_cast<const uint4*>(rec + s * 2 * R + 16 * v);
-  }
+  size_t at;
+  int in_tile;
+  if (w4_tile_record(e, n0, k0, K, N, R, at, in_tile))
+    for (int v = 16 * (threadIdx.x & 31); v < R; v += 512)
+      *reinterpret_cast<uint4*>(packed + at + v) = *reinterpret_cast<const uint4*>(rec + in_tile + v);
 }
 
 // codes uint8 [E][N][K/2] (element 2b in the low nibble of byte b), scales bf16 [E][N][G],
@@ -90,7 +100,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
     const size_t at = (size_t)e * N + n;
     const uint4 raw = __ldg(reinterpret_cast<const uint4*>(codes + at * (K / 2) + k / 2));
     const int strip = row >> 4, r = row & 15, block = part >> 1, half = part & 1;
-    uint8_t* b = rec + (strip * 2 + block) * R;
+    uint8_t* b = rec + (strip * 2 + block) * w4_tile_pitch(R);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -141,7 +151,6 @@ __device__ __forceinline__ W4Zero w4_zero(uint32_t zero) {
 
 // A tile of bf16 weights in shared memory, [128 along K][64 rows], 8 elements of padding.  In the
 // two kernels below a thread has 16 elements along K of two neighbouring rows.
-constexpr int W4_TILE_PITCH = W4_TILE_N + 8;
 __device__ __forceinline__ uint32_t* w4_word(uint8_t* rec, int R, int row, int part, int i) {
   const int r = row & 15;
   return reinterpret_cast<uint32_t*>(rec + ((row >> 4) * 2 + (part >> 2)) * R +
@@ -149,6 +158,27 @@ __device__ __forceinline__ uint32_t* w4_word(uint8_t* rec, int R, int row, int p
                                      4 * (r >> 3));
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 w4_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 w4_add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 // rint(x / s) with the correctly rounded quotient; 0 for s = 0.  Out of line: rarely needed.
 __device__ __noinline__ float w4_rounded_quotient(float x, float s) {
   return s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
@@ -160,38 +190,37 @@ __device__ __noinline__ float w4_rounded_quotient(float x, float s) {
 // clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15).  A zero scale
 // gives codes and zero points of 8.
 //
-// Bound by its bytes (2.5 to 2.6 per weight) once the arithmetic is short: the tile comes and
-// goes in 16-byte vectors; the division is a multiplication by the reciprocal, within 2^-19 of the
+// Bound by its instructions (11 a weight), then its bytes (2.5 to 2.6 a weight): a warp reads two
+// rows a lane, whole lines along N, straight into registers (through shared memory it took 169 us for
+// 128 matrices of 2816 x 704, so 143: 4.5 TB/s); 48 registers keep 40 warps on an SM (63 did with
+// zero points: 172 us, so 160); the division is a multiplication by the reciprocal, within 2^-19 of the
 // quotient (at most 16); adding 1.5 * 2^23 rounds to an integer in the low bits, and eight of those
 // add up to a packed word when the constant parts are taken off at the end.  The product rounds
-// like the quotient once it has been rounded to a multiple of 2^-11: a weight a 2^i and a scale
-// b 2^j have 8-bit a and b, so a quotient either is a half-integer h or differs from it by at
-// least 2^(j-2) / (b 2^j) > 2^-10.
+// like the quotient once it has been rounded to a multiple of 2^-11 (fused with the product, by an
+// addend of 1.5 * 2^12, which the second addition takes off again): a weight a 2^i and a scale b 2^j
+// have 8-bit a and b, so a quotient either is a half-integer h or differs from it by at least
+// 2^(j-2) / (b 2^j) > 2^-10.
 template <bool ZP>
-__global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K,
+__global__ void __launch_bounds__(256, 5) w4_quantize_kernel(const __nv_bfloat16* __restrict__ w, int K,
                                                           int N, int group,
                                                           uint8_t* __restrict__ packed) {
-  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
   __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
   __shared__ __nv_bfloat162 s_lo[8][32], s_hi[8][32];
-  const int R = w4_record(group, ZP), gpb = w4_groups(group);
+  const int R = w4_record(group, ZP), pitch = w4_tile_pitch(R), gpb = w4_groups(group);
   const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
-  const __nv_bfloat16* src = w + ((size_t)e * K + k0) * N + n0;
-#pragma unroll
-  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
-    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
-    if (k0 + k < K && n0 + 8 * v < N)
-      *reinterpret_cast<uint4*>(&tile[k][8 * v]) = __ldg(reinterpret_cast<const uint4*>(src + (size_t)k * N + 8 * v));
-  }
-  __syncthreads();
   const int pair = threadIdx.x & 31, part = threadIdx.x >> 5;   // rows 2 pair, + 1; k 16 part .. + 15
   const bool in = n0 + 2 * pair < N && k0 + 16 * part < K;
+  const __nv_bfloat16* src = w + ((size_t)e * K + k0 + 16 * part) * N + n0 + 2 * pair;
   __nv_bfloat162 v[16];
   __nv_bfloat162 lo = __float2bfloat162_rn(0.f), hi = lo;
   if (in) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      v[i] = *reinterpret_cast<const __nv_bfloat162*>(&tile[16 * part + i][2 * pair]);
+      const uint32_t two = __ldg(reinterpret_cast<const uint32_t*>(src + (size_t)i * N));
+      v[i] = *reinterpret_cast<const __nv_bfloat162*>(&two);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
       lo = __hmin2(lo, v[i]);
       hi = __hmax2(hi, v[i]);
     }
@@ -205,48 +234,60 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* _
       lo = __hmin2(lo, s_lo[i][pair]);
       hi = __hmax2(hi, s_hi[i][pair]);
     }
+    constexpr float SNAP = 6144.f;                        // 1.5 * 2^12
+    constexpr float ROUND = 12582912.f;                   // 1.5 * 2^23
+    constexpr uint32_t BITS = 0x4B400000u;                // its bits
+    __nv_bfloat16 sb[2];
+    float s[2], inv[2];
+    int z[2];
+    uint32_t word[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float l = c ? __high2float(lo) : __low2float(lo), h = c ? __high2float(hi) : __low2float(hi);
+      sb[c] = __float2bfloat16_rn(ZP ? __fdiv_rn(__fsub_rn(h, l), 15.f) : __fdiv_rn(fmaxf(-l, h), 7.f));
+      s[c] = __bfloat162float(sb[c]);
+      inv[c] = __fdiv_rn(1.f, s[c]);
+      z[c] = ZP && s[c] > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(-l, s[c])), 0.f), 15.f) : 8;
+      word[c][0] = word[c][1] = ((uint32_t)z[c] - BITS) * 0x11111111u;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x2 = *reinterpret_cast<const uint32_t*>(&v[i]);
+      float2 q = w4_fma2(make_float2(__uint_as_float(x2 << 16), __uint_as_float(x2 & 0xffff0000u)),
+                         make_float2(inv[0], inv[1]), make_float2(SNAP, SNAP));
+      q = w4_add2(q, make_float2(ROUND - SNAP, ROUND - SNAP));
+      uint32_t bits[2] = {__float_as_uint(q.x), __float_as_uint(q.y)};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        // the rounding of the scale can leave the largest quotient at 16 - zero
+        if (ZP) bits[c] = min(bits[c], BITS + 15u - (uint32_t)z[c]);
+        word[c][i >> 3] += bits[c] << (4 * (((i & 7) >> 1) + 4 * (i & 1)));
+      }
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int row = 2 * pair + c;
-      const float l = c ? __high2float(lo) : __low2float(lo), h = c ? __high2float(hi) : __low2float(hi);
-      const __nv_bfloat16 sb = __float2bfloat16_rn(ZP ? __fdiv_rn(__fsub_rn(h, l), 15.f)
-                                                      : __fdiv_rn(fmaxf(-l, h), 7.f));
-      const float s = __bfloat162float(sb), inv = __fdiv_rn(1.f, s);
-      const int z = ZP && s > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(-l, s)), 0.f), 15.f) : 8;
-      constexpr float ROUND = 12582912.f;             // 1.5 * 2^23
-      constexpr uint32_t BITS = 0x4B400000u;          // its bits
-      constexpr float SNAP = 6144.f;                  // 1.5 * 2^12
-      uint32_t word[2] = {((uint32_t)z - BITS) * 0x11111111u, ((uint32_t)z - BITS) * 0x11111111u};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float x = c ? __high2float(v[i]) : __low2float(v[i]);
-        const float m = __fsub_rn(__fadd_rn(__fmul_rn(x, inv), SNAP), SNAP);
-        uint32_t bits = __float_as_uint(__fadd_rn(m, ROUND));
-        // the rounding of the scale can leave the largest quotient at 16 - zero
-        if (ZP) bits = min(bits, BITS + 15u - (uint32_t)z);
-        word[i >> 3] += bits << (4 * (((i & 7) >> 1) + 4 * (i & 1)));
-      }
-      if (!(s > 1e-30f && s < 1e30f)) {   // the reciprocal or a subnormal: by division
+      if (!(s[c] > 1e-30f && s[c] < 1e30f)) {   // the reciprocal or a subnormal: by division
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
           uint32_t exact = 0;
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
-            const float x = __bfloat162float(tile[16 * part + 8 * u + i][row]);
-            const float q = w4_rounded_quotient(x, s) + (float)z;
+            const float x = __bfloat162float(src[(size_t)(8 * u + i) * N + c]);
+            const float q = w4_rounded_quotient(x, s[c]) + (float)z[c];
             exact |= (uint32_t)(int)fminf(fmaxf(q, 0.f), 15.f) << (4 * ((i >> 1) + 4 * (i & 1)));
           }
-          if (u) word[1] = exact;
-          else word[0] = exact;
+          if (u) word[c][1] = exact;
+          else word[c][0] = exact;
         }
       }
-      *w4_word(rec, R, row, part, 0) = word[0];
-      *w4_word(rec, R, row, part, 1) = word[1];
+      *w4_word(rec, pitch, row, part, 0) = word[c][0];
+      *w4_word(rec, pitch, row, part, 1) = word[c][1];
       if ((part & (gpb == 2 ? 1 : 3)) == 0) {
-        uint8_t* b = rec + ((row >> 4) * 2 + (part >> 2)) * R;
+        uint8_t* b = rec + ((row >> 4) * 2 + (part >> 2)) * pitch;
         const int at = ((part >> 1) & (gpb - 1)) * 16 + w4_row_slot(row & 15);
-        reinterpret_cast<__nv_bfloat16*>(b + 512)[at] = sb;
-        if (ZP) b[512 + gpb * 32 + at] = (uint8_t)z;
+        reinterpret_cast<__nv_bfloat16*>(b + 512)[at] = sb[c];
+        if (ZP) b[512 + gpb * 32 + at] = (uint8_t)z[c];
       }
     }
   }
@@ -254,23 +295,22 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16* _
   w4_store_tile(rec, packed, e, n0, k0, K, N, R);
 }
 
-// packed -> bf16 w [E][K][N]: each value rounded once.  Bound by its bytes: codes are decoded in
-// pairs as the products do (a quarter of the difference, exact), times 4, times the scale.
+// packed -> bf16 w [E][K][N]: each value rounded once.  Bound by its bytes (110 us, 5.9 TB/s, for
+// 128 matrices of 2816 x 704 with groups of 32): codes are decoded in pairs as the products do (a
+// quarter of the difference, exact), times 4, times the scale, and a warp writes whole lines from
+// registers.
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __restrict__ packed, int K,
                                                             int N, int group, int zeros,
                                                             __nv_bfloat16* __restrict__ w) {
-  __shared__ __align__(16) __nv_bfloat16 tile[W4_TILE_K][W4_TILE_PITCH];
   __shared__ __align__(16) uint8_t rec[W4_TILE_BYTES];
-  const int R = w4_record(group, zeros), gpb = w4_groups(group);
+  const int R = w4_record(group, zeros), pitch = w4_tile_pitch(R), gpb = w4_groups(group);
   const int n0 = blockIdx.x * W4_TILE_N, k0 = blockIdx.y * W4_TILE_K, e = blockIdx.z;
   const int strips = min(4, (N - n0) / W4_ROWS), blocks = min(2, (K - k0) / W4_KB);
-  const int vec = blocks * R / 16;
-  for (int i = threadIdx.x; i < strips * vec; i += 256) {
-    const int s = i / vec, v = i - s * vec;
-    const uint8_t* src =
-        packed + (((size_t)e * (N / W4_ROWS) + n0 / W4_ROWS + s) * (K / W4_KB) + k0 / W4_KB) * R;
-    *reinterpret_cast<uint4*>(rec + s * 2 * R + 16 * v) = __ldg(reinterpret_cast<const uint4*>(src) + v);
-  }
+  size_t from;
+  int in_tile;
+  if (w4_tile_record(e, n0, k0, K, N, R, from, in_tile))
+    for (int v = 16 * (threadIdx.x & 31); v < R; v += 512)
+      *reinterpret_cast<uint4*>(rec + in_tile + v) = __ldg(reinterpret_cast<const uint4*>(packed + from + v));
   __syncthreads();
   const int pair = threadIdx.x & 31, part = threadIdx.x >> 5;
   if (2 * pair < 16 * strips && part < 4 * blocks) {
@@ -278,14 +318,14 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __res
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int row = 2 * pair + c;
-      const uint8_t* b = rec + ((row >> 4) * 2 + (part >> 2)) * R;
+      const uint8_t* b = rec + ((row >> 4) * 2 + (part >> 2)) * pitch;
       const int at = ((part >> 1) & (gpb - 1)) * 16 + w4_row_slot(row & 15);
       const uint32_t s2 = reinterpret_cast<const uint16_t*>(b + 512)[at] * 0x00010001u;
       const W4Zero z = w4_zero(zeros ? b[512 + gpb * 32 + at] : 8u);
       const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2), four = __float2bfloat162_rn(4.f);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t word = *w4_word(rec, R, row, part, u);
+        const uint32_t word = *w4_word(rec, pitch, row, part, u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t d = i & 1 ? w4_high(word >> (4 * (i - 1)), z) : w4_low(word >> (4 * i), z);
@@ -294,19 +334,12 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint8_t* __res
         }
       }
     }
+    __nv_bfloat16* dst = w + ((size_t)e * K + k0 + 16 * part) * N + n0 + 2 * pair;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      *reinterpret_cast<uint32_t*>(&tile[16 * part + 2 * i][2 * pair]) = __byte_perm(val[0][i], val[1][i], 0x5410);
-      *reinterpret_cast<uint32_t*>(&tile[16 * part + 2 * i + 1][2 * pair]) = __byte_perm(val[0][i], val[1][i], 0x7632);
+      *reinterpret_cast<uint32_t*>(dst + (size_t)(2 * i) * N) = __byte_perm(val[0][i], val[1][i], 0x5410);
+      *reinterpret_cast<uint32_t*>(dst + (size_t)(2 * i + 1) * N) = __byte_perm(val[0][i], val[1][i], 0x7632);
     }
-  }
-  __syncthreads();
-  __nv_bfloat16* dst = w + ((size_t)e * K + k0) * N + n0;
-#pragma unroll
-  for (int u = 0; u < W4_TILE_K * W4_TILE_N / 8 / 256; ++u) {
-    const int i = threadIdx.x + 256 * u, k = i / (W4_TILE_N / 8), v = i % (W4_TILE_N / 8);
-    if (k0 + k < K && n0 + 8 * v < N)
-      *reinterpret_cast<uint4*>(dst + (size_t)k * N + 8 * v) = *reinterpret_cast<const uint4*>(&tile[k][8 * v]);
   }
 }
 
