@@ -396,9 +396,10 @@ moe_status_t moe_dense_ffn_w4(const void *x, const void *w_gate, const void *w_u
 
 /*
  * moe_forward_w4 -- the routed layer with 4-bit expert weights for batches of T <= 16 tokens.
- * Router as moe_route (bf16 w_router; the same ids and weights), experts as moe_forward: w_gate,
- * w_up E packed matrices (K = H, N = I), w_down E packed matrices (K = I, N = H).  h is rounded
- * to bf16; the expert outputs and their weighted sum stay in fp32 until y.  flags:
+ * Router as moe_route (bf16 w_router; the same ids, and weights within 1e-6 of its own: the softmax
+ * is taken in fp32 of the fp64 logits' differences), experts as moe_forward: w_gate, w_up E packed
+ * matrices (K = H, N = I), w_down E packed matrices (K = I, N = H).  h is rounded to bf16; the
+ * expert outputs and their weighted sum stay in fp32 until y.  flags:
  * MOE_FLAG_NO_RENORM, MOE_FLAG_W4_ZEROS.  aux as moe_forward.  Shapes as moe_forward, T <= 16.
  * Workspace: moe_w4_workspace_size bytes (0 = unsupported shape).
  */

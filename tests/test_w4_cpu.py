@@ -164,6 +164,25 @@ def test_binding_refuses_without_a_device(lib):
             call()
 
 
+def test_reciprocal_products_round_like_quotients():
+    """The quantiser multiplies by the reciprocal, in one fused operation that also rounds to a
+    multiple of 2^-11, and then rounds to an integer: for every pair of 8-bit significands and every
+    exponent that gives a quotient up to 16 that is the rounded quotient, ties included."""
+    f32 = np.float32
+    snap, rnd = 1.5 * 2.0 ** 12, 1.5 * 2.0 ** 23
+    a = np.arange(128, 256, dtype=np.float64)[:, None]
+    for b in range(128, 256):
+        inv = f32(1) / f32(b)
+        for e in range(-8, 5):
+            x = a * 2.0 ** e
+            x = x[x / b <= 16]
+            # the product has 32 bits and the sum ends above 2^-29 of it: exact in float64 until it is
+            # rounded to fp32, as the fused operation does
+            snapped = (x * np.float64(inv) + snap).astype(f32)
+            got = (snapped.astype(np.float64) + (rnd - snap)).astype(f32).astype(np.float64) - rnd
+            assert np.array_equal(got, np.rint(x / b))
+
+
 def test_packed_reference_round_trip():
     """Every code, scale and zero point of the reference packing is where the header says."""
     codes, scales, zp = ref.make_checkpoint(1, 128, 32, 32, True, seed=3)

@@ -66,6 +66,37 @@ def test_quantize_takes_the_documented_steps(E, K, N, group, zeros):
     synced()
 
 
+def test_quantize_rounds_ties_to_even():
+    """Weights at half-integer multiples of the scale, all exact in bf16, at three scales."""
+    K, N = 128, 16
+    w = torch.zeros((1, K, N), dtype=torch.float64)
+    steps = torch.tensor([7.0] + [j + 0.5 for j in range(-7, 7)] + [-7.0])
+    for n in range(N):
+        scale = (1.0, 1.5, 1.25)[n % 3] * 2.0 ** (n - 12)
+        w[0, :, n] = scale * steps.repeat(K // 16)
+    assert torch.equal(w.to(torch.bfloat16).double(), w)
+    w = w.to(torch.bfloat16)
+    for group in (32, 64, 128):
+        codes, scales, _ = ref.quantize(w, group, False)
+        assert torch.equal(codes[0, :, 1:15].double(), 8 + torch.round(steps[1:15].double()).expand(N, 14))
+        q = moe.w4_quantize(w.cuda(), group=group)
+        assert np.array_equal(q.data.cpu().numpy(), ref.packed_bytes(codes, scales, None, group))
+
+
+def test_quantize_ragged_tiles():
+    """Matrices that end inside a tile of 64 rows x 128 elements, several of them."""
+    g = torch.Generator().manual_seed(6)
+    for E, K, N in ((2, 64, 16), (3, 192, 48), (1, 320, 1040)):
+        w = torch.randn((E, K, N), generator=g).to(torch.bfloat16)
+        for zeros in (False, True):
+            codes, scales, zp = ref.quantize(w, 128, zeros)
+            q = moe.w4_quantize(w.cuda(), group=128, zeros=zeros)
+            assert np.array_equal(q.data.cpu().numpy(),
+                                  ref.packed_bytes(codes, scales, zp if zeros else None, 128))
+            assert torch.equal(moe.w4_dequantize(q).cpu(),
+                               ref.values(codes, scales, zp if zeros else None, 128).to(torch.bfloat16))
+
+
 def test_one_matrix_may_leave_the_leading_axis_out():
     c, s, z = ref.make_checkpoint(1, 128, 32, 64, True, seed=1)
     a = moe.w4_pack(ref.nibbles(c)[0].cuda(), s[0].cuda(), z[0].cuda(), group=64)
@@ -98,6 +129,30 @@ def test_linear_sizes(T, K, N, group, zeros):
     ref.check(moe.linear_w4(x.cuda(), w, fp32=True), y, err)
     ref.check(moe.linear_w4(x.cuda(), w), y, err)
     synced()
+
+
+@pytest.mark.parametrize("T,K,N", [
+    # K shared by 2, 4 and 8 CTAs, with odd last strips and uneven shares of K; rows kept in shared
+    # memory and fragments; more units than run at once
+    (1, 704, 2816), (4, 1088, 4112), (6, 4160, 1040), (8, 8256, 528), (2, 16320, 112),
+    (12, 16384, 2064), (9, 1984, 4112), (16, 704, 2832), (13, 8192, 4096), (5, 576, 50000),
+    (8, 4160, 20016), (10, 1024, 32784)])
+def test_linear_cuts(T, K, N):
+    w, v = matrix(1, K, N, 64, False, seed=K + N)
+    x = rows(T, K, N)
+    y, err = ref.linear(x, v[0], 64)
+    ref.check(moe.linear_w4(x.cuda(), w, fp32=True), y, err)
+    synced()
+
+
+def test_linear_same_call_same_bits():
+    """Sums are joined in a fixed order, whichever CTA takes a unit."""
+    for T, K, N in ((1, 2816, 65536), (16, 2816, 40000), (8, 8192, 1024), (3, 704, 2816)):
+        w, _ = matrix(1, K, N, 128, False, seed=T)
+        x = rows(T, K, T).cuda()
+        first = moe.linear_w4(x, w, fp32=True)
+        for _ in range(20):
+            assert torch.equal(moe.linear_w4(x, w, fp32=True), first)
 
 
 def test_linear_one_hot_rows_give_the_weights():
@@ -174,7 +229,8 @@ def test_linear_past_32_bits():
 @pytest.mark.parametrize("T,H,I,group,zeros", [
     (1, 64, 64, 32, False), (16, 64, 64, 128, True), (1, 2816, 2112, 64, False),
     (8, 2816, 2112, 32, True), (16, 2816, 2112, 128, False), (5, 192, 1088, 64, True),
-    (9, 4096, 128, 32, False), (3, 128, 8192, 128, True)])
+    (9, 4096, 128, 32, False), (3, 128, 8192, 128, True), (8, 192, 8192, 64, False),
+    (8, 8192, 192, 64, True), (13, 1088, 2752, 128, False), (2, 16384, 64, 64, False)])
 def test_dense_ffn(T, H, I, group, zeros):
     g, vg = matrix(1, H, I, group, zeros, seed=1)
     u, vu = matrix(1, H, I, group, zeros, seed=2)
@@ -214,7 +270,11 @@ LAYER_CASES = [
     (8, 256, 128, 128, 8, 64, False, True, True), (9, 192, 64, 64, 8, 32, False, False, True),
     (16, 256, 8, 128, 2, 128, True, True, False), (16, 128, 256, 64, 8, 64, True, False, True),
     (13, 320, 132 + 4, 192, 5, 32, True, True, True), (7, 2816, 32, 704, 8, 64, False, False, True),
-    (16, 4096, 4, 64, 4, 64, False, False, True)]
+    (16, 4096, 4, 64, 4, 64, False, False, True),
+    # taller units of gate | up, and of W_down with an odd tail: many rows an expert, and few
+    (16, 128, 8, 2432, 4, 64, False, False, True), (12, 4800, 16, 64, 8, 32, True, False, True),
+    (16, 64, 256, 448, 8, 128, False, False, True), (16, 2048, 128, 64, 8, 64, False, False, True),
+    (8, 128, 8, 2432, 4, 32, True, True, False)]
 
 
 @pytest.mark.parametrize("T,H,E,I,k,group,zeros,bias,renorm", LAYER_CASES)
