@@ -31,7 +31,10 @@ namespace moe {
 constexpr int W4S_MMA_WARPS = 8, W4S_EPI_WARPS = 2;
 constexpr int W4S_THREADS = 32 * (W4S_MMA_WARPS + W4S_EPI_WARPS + 1);
 constexpr int W4S_EPI_THREADS = 32 * W4S_EPI_WARPS;
-constexpr int W4S_STAGES = 3;
+// Two large stages: what the roles do once a chunk costs more than the finer overlap of three or four
+// smaller ones gives (T = 16, 2816 x 131072: 67 us with two, 70 with three, 78 with four; the routed
+// layer at 16 tokens 102 and 112).
+constexpr int W4S_STAGES = 2;
 constexpr int W4S_COL = 20;             // floats per accumulator column (16 rows, padded)
 constexpr int W4S_SMEM = 115712;        // two CTAs per SM
 // accumulator tile: 16 (K slice, strip) pairs x 8 NB columns
