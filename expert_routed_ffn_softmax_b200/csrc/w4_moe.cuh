@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
           }
           fence_proxy_async_global();
           W4Pos p = from;
-          for (int i = 0; i < n && ok; ++i, p.next()) activations(i * step, p.s);
+          // also when giving up: the chunks were announced with their activations
+          for (int i = 0; i < n; ++i, p.next()) activations(i * step, p.s);
           b = n * step;
         }
         for (; b < kb && ok; b += step) {

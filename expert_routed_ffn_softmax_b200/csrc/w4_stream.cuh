@@ -4,8 +4,9 @@
 //
 // What bounds it.  At T <= 16 a weight byte meets at most 64 flops, so the work is reading the
 // weights once at the memory's rate, decoding two weights per byte on the way: per SM about 23
-// bytes (46 weights) a clock.  The decode and the products of a block (1024 weights) take 23 to 25
-// clocks of an SM (measured by repeating them), its bytes 22 to 24: both must run at once.
+// bytes (46 weights) a clock.  The decode and the products of a block (1024 weights) take 24 clocks
+// of an SM, 35 with two row tiles (measured by repeating them), its bytes 22: both must run at once,
+// and do to two thirds (2816 x 131072 in 46 us for one row, 68 for 16; the bytes alone 30).
 //
 // Roles of a CTA (two CTAs per SM, so that one multiplies while the other joins or waits):
 //   producer     one thread copies each unit in chunks of consecutive blocks, one bulk copy per
@@ -71,14 +72,14 @@ __device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity, const vo
 // Barriers and flags of a CTA.
 struct W4Sync {
   uint32_t base;
-  volatile int* flags;   // {abort, phases issued (chunks, the end), -, activations issued}
+  volatile int* flags;   // {abort, phases issued (chunks, the end), activations issued}
   __device__ uint32_t full(int s) const { return base + 8u * s; }
   __device__ uint32_t empty(int s) const { return base + 8u * (W4S_STAGES + s); }
   __device__ uint32_t acc_full(int b) const { return base + 8u * (2 * W4S_STAGES + b); }
   __device__ uint32_t acc_empty(int b) const { return base + 8u * (2 * W4S_STAGES + 2 + b); }
   __device__ uint32_t act_full() const { return base + 8u * (2 * W4S_STAGES + 4); }
   __device__ uint32_t steal_full() const { return base + 8u * (2 * W4S_STAGES + 5); }
-  static constexpr int BYTES = 8 * (2 * W4S_STAGES + 6) + 16;   // 112
+  static constexpr int BYTES = 8 * (2 * W4S_STAGES + 6) + 16;
   __device__ void init(uint8_t* at) {
     base = smem_u32(at);
     flags = reinterpret_cast<volatile int*>(at + 8 * (2 * W4S_STAGES + 6));
@@ -95,7 +96,7 @@ struct W4Sync {
     }
     mbar_init(act_full(), 1);
     mbar_init(steal_full(), 1);
-    flags[0] = flags[1] = flags[2] = flags[3] = 0;
+    flags[0] = flags[1] = flags[2] = 0;
     fence_barrier_init();
   }
   __device__ void abort() const { flags[0] = 1; }
@@ -106,7 +107,7 @@ struct W4Sync {
   __device__ void drain() const {
     for (int q = max(0, flags[1] - W4S_STAGES); q < flags[1]; ++q)
       mbar_wait_ns(full(q % W4S_STAGES), (q / W4S_STAGES) & 1, kDrainLimitNs);
-    if (flags[3]) mbar_wait_ns(act_full(), 0, kDrainLimitNs);
+    if (flags[2]) mbar_wait_ns(act_full(), 0, kDrainLimitNs);
   }
 };
 
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
       auto activations = [&](int chunks) {
         fence_proxy_async_global();
         if (!a.frag) {
-          sy.flags[3] = 1;
+          sy.flags[2] = 1;
           mbar_arrive_expect_tx(sy.act_full(), a.T * 128 * blocks);
           for (int t = 0; t < a.T; ++t)
             bulk_load(smem_u32(w4sm + SL.act) + t * act_pitch, a.act + (size_t)t * a.K + 64 * k0, 128 * blocks,

@@ -444,6 +444,27 @@ def test_two_threads_at_once():
     synced()
 
 
+def test_waits_that_run_out_are_reported():
+    """With the wait limit at next to nothing the layer's hand-overs run out: the call returns, the
+    error is reported once, and the next call is right again."""
+    T, H, E, I, k = 8, 256, 64, 128, 4
+    q, _, wr, _ = layer_inputs(T, H, E, I, 64, False, seed=90)
+    x, wr = rows(T, H, 90).cuda(), wr.cuda()
+    want = moe.forward_w4(x, wr, *q, k)
+    synced()
+    lib = moe.load()
+    assert lib.moe_debug_set_wait_limit_ns(1) == 0
+    try:
+        moe.forward_w4(x, wr, *q, k)
+        status = moe.sync_status()
+    finally:
+        assert lib.moe_debug_set_wait_limit_ns(0) == 0
+    assert status == _abi.MOE_ERR_TIMEOUT
+    synced()
+    assert torch.equal(moe.forward_w4(x, wr, *q, k), want)
+    synced()
+
+
 def test_stream_argument():
     """stream=: the call and what it allocates belong to that stream."""
     x, wr, experts, dense, head, k = block_inputs(seed=7)
