@@ -8,6 +8,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -500,10 +501,15 @@ _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice
     torch.cuda.current_device
 
 
-def _raw_stream(index: int) -> int:
-    """The device's current stream as an integer (the calls below last a few microseconds, so the
-    way to it is short)."""
-    return torch._C._cuda_getCurrentRawStream(index)
+# The device's current stream as an integer (the calls below last a few microseconds, so the way to
+# it is short).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+@functools.lru_cache(maxsize=256)
+def _w4_bytes(call: str, *sizes: int) -> int:
+    """What one of the size queries below says, which depends on sizes and flags alone."""
+    return getattr(load(), call)(*sizes)
 
 
 def _elsewhere(fn, first, stream, args):
@@ -554,7 +560,7 @@ def _rows(x, name: str):
 
 
 def _w4_empty(E: int, K: int, N: int, group: int, zeros: bool, like) -> W4Weights:
-    n = load().moe_w4_packed_bytes(E, K, N, group, MOE_FLAG_W4_ZEROS if zeros else 0)
+    n = _w4_bytes("moe_w4_packed_bytes", E, K, N, group, MOE_FLAG_W4_ZEROS if zeros else 0)
     if n == 0:
         raise MoEError(MOE_ERR_UNSUPPORTED if group in (32, 64, 128) else MOE_ERR_INVALID_ARG,
                        "moe_w4_packed_bytes")
@@ -595,13 +601,12 @@ def w4_quantize(w: torch.Tensor, group: int = 64, zeros: bool = False, stream=No
         raise TypeError("w must be a CUDA tensor")
     if stream is not None or not _here(w):
         return _elsewhere(w4_quantize, w, stream, (w, group, zeros))
-    if w.dim() == 2:
-        w = w.unsqueeze(0)
-    if w.dim() != 3:
-        raise ValueError(f"w must be [E, K, N] or [K, N], got {tuple(w.shape)}")
-    E, K, N = w.shape
+    shape = w.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"w must be [E, K, N] or [K, N], got {tuple(shape)}")
+    E, K, N = shape if len(shape) == 3 else (1, *shape)
     dev = w.get_device()
-    pw = _tensor(w, "w", _BF16, (E, K, N), dev)
+    pw = _tensor(w, "w", _BF16, shape, dev)
     q = _w4_empty(E, K, N, group, zeros, w)
     _check(load().moe_w4_quantize_weights(pw, E, K, N, group, q.flags, q.data.data_ptr(),
                                           _raw_stream(dev)), "moe_w4_quantize_weights")
@@ -645,9 +650,9 @@ def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, fp
     """moe_linear_w4: y = x W for x bf16 [T, K], T <= 16, and one 4-bit matrix -> y [T, N], bf16
     (or fp32 with fp32=True).  stream: run on that stream instead of the current one."""
     T, K = _rows(x, "x")
-    if stream is not None or not _here(x):
-        return _elsewhere(linear_w4, x, stream, (x, w, out, fp32, workspace_buf))
     dev = x.get_device()
+    if stream is not None or dev != _current_device():
+        return _elsewhere(linear_w4, x, stream, (x, w, out, fp32, workspace_buf))
     N = w.N if type(w) is W4Weights else 0
     pw = _w4(w, "w", 1, K, N, dev)
     px = _tensor(x, "x", _BF16, (T, K), dev)
@@ -660,20 +665,15 @@ def linear_w4(x: torch.Tensor, w: W4Weights, out: torch.Tensor | None = None, fp
     if T == 0:
         return out
     L = _lib or load()
-    pws = n = 0
-    if T * K >= _W4_WORKSPACE_FROM:
-        n = L.moe_linear_w4_workspace_size(T, K)
-        if n:
-            pws, n, _own = _w4_workspace(n, workspace_buf, "", x)
+    pws = 0
+    n = _w4_bytes("moe_linear_w4_workspace_size", T, K)
+    if n:
+        pws, n, _own = _w4_workspace(n, workspace_buf, "", x)
     rc = L.moe_linear_w4(px, pw, T, K, N, w.group, w.flags | MOE_FLAG_F32_OUT if fp32 else w.flags, py,
                          pws, n, _raw_stream(dev))
     if rc:
         _check(rc, "moe_linear_w4")
     return out
-
-
-# moe_linear_w4_workspace_size is 0 for fewer elements (and T <= 8)
-_W4_WORKSPACE_FROM = 512
 
 
 def dense_ffn_w4(x: torch.Tensor, w_gate: W4Weights, w_up: W4Weights, w_down: W4Weights,
@@ -683,9 +683,9 @@ def dense_ffn_w4(x: torch.Tensor, w_gate: W4Weights, w_up: W4Weights, w_down: W4
     y = (gelu_tanh(x W_gate) * (x W_up)) W_down.  stream: run on that stream instead of the current
     one."""
     T, H = _rows(x, "x")
-    if stream is not None or not _here(x):
-        return _elsewhere(dense_ffn_w4, x, stream, (x, w_gate, w_up, w_down, out, workspace_buf))
     dev = x.get_device()
+    if stream is not None or dev != _current_device():
+        return _elsewhere(dense_ffn_w4, x, stream, (x, w_gate, w_up, w_down, out, workspace_buf))
     I = w_gate.N if type(w_gate) is W4Weights else 0
     pg = _w4(w_gate, "w_gate", 1, H, I, dev)
     pu = _w4(w_up, "w_up", 1, H, I, dev)
@@ -700,7 +700,7 @@ def dense_ffn_w4(x: torch.Tensor, w_gate: W4Weights, w_up: W4Weights, w_down: W4
     if T == 0:
         return out
     L = _lib or load()
-    pws, n, _own = _w4_workspace(L.moe_dense_w4_workspace_size(T, H, I), workspace_buf,
+    pws, n, _own = _w4_workspace(_w4_bytes("moe_dense_w4_workspace_size", T, H, I), workspace_buf,
                                  "moe_dense_w4_workspace_size", x)
     rc = L.moe_dense_ffn_w4(px, pg, pu, pd, T, H, I, w_gate.group, w_gate.flags, py, pws, n,
                             _raw_stream(dev))
@@ -717,11 +717,11 @@ def forward_w4(x: torch.Tensor, w_router: torch.Tensor, w_gate: W4Weights, w_up:
     [T, H] (and the routing dict of forward if aux).  stream: run on that stream instead of the
     current one."""
     T, H = _rows(x, "x")
-    if stream is not None or not _here(x):
+    dev = x.get_device()
+    if stream is not None or dev != _current_device():
         return _elsewhere(forward_w4, x, stream, (x, w_router, w_gate, w_up, w_down, k, bias, renorm,
                                                   aux, out, workspace_buf))
     E = _rows(w_router, "w_router")[1]
-    dev = x.get_device()
     I = w_gate.N if type(w_gate) is W4Weights else 0
     pg = _w4(w_gate, "w_gate", E, H, I, dev)
     pu = _w4(w_up, "w_up", E, H, I, dev)
@@ -740,7 +740,7 @@ def forward_w4(x: torch.Tensor, w_router: torch.Tensor, w_gate: W4Weights, w_up:
         return (out, aux_d) if aux else out
     L = _lib or load()
     flags = w_gate.flags if renorm else w_gate.flags | MOE_FLAG_NO_RENORM
-    pws, n, _own = _w4_workspace(L.moe_w4_workspace_size(T, H, E, I, k, flags), workspace_buf,
+    pws, n, _own = _w4_workspace(_w4_bytes("moe_w4_workspace_size", T, H, E, I, k, flags), workspace_buf,
                                  "moe_w4_workspace_size", x)
     rc = L.moe_forward_w4(px, pr, pb, pg, pu, pd, T, H, E, I, k, w_gate.group, flags, py,
                           None if a is None else ctypes.byref(a), pws, n, _raw_stream(dev))

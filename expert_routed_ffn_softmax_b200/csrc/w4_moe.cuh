@@ -517,8 +517,11 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_moe_kernel(const __grid_con
           uint32_t dst = ring + s * STAGE;
           mbar_arrive_expect_tx(sy.full(s), strips * bytes + row_bytes * min(step, kb - b));
           if (down) {
+            // strips whose whole depth is one chunk are one run of bytes
             const uint8_t* src = a.wd + w_at + (size_t)b * R;
-            for (int i = 0; i < strips; ++i, src += pitch, dst += bytes) bulk_load(dst, src, bytes, sy.full(s));
+            if (step >= kb) bulk_load(dst, src, strips * bytes, sy.full(s));
+            for (int i = 0; step < kb && i < strips; ++i, src += pitch, dst += bytes)
+              bulk_load(dst, src, bytes, sy.full(s));
           } else {
             size_t from = w_at + (size_t)b * R;
             for (int i = 0; i < strips; i += 2, from += pitch, dst += 2 * bytes) {
