@@ -42,8 +42,8 @@ int w4_slots(const DeviceState& d) { return 2 * std::max(1, d.num_sms); }
 // with one (45 for two row tiles); its bytes at 22 a ns (32 for a CTA alone on its SM, without
 // fragments); its copies at 100 each.  Per cluster 400 a CTA (200 with fragments, whose own launch
 // hides its start) and 0.3 for every sum exchanged.  Over 17 shapes (T 1 to 16, K 704 to 16384, N
-// 704 to 131072) and all 16 cuts of each, timed one by one, the choice was within 8 % of the best (16 % at
-// T = 12, 16384 x 2048).
+// 704 to 131072) and all 16 cuts of each, timed one by one, the choice was within 8 % of the best
+// (18 % at T = 12, 16384 x 2048).
 struct W4Plan {
   int lg = 0, cluster = 1, units = 0, step = 0, stage = 0, smem = 0, frag = 0;
 };
@@ -68,9 +68,11 @@ W4Plan w4_plan(int mode, int T, int K, int N, int record, int sms) {
       p.lg = lg;
       p.cluster = cluster;
       p.units = (N / W4_ROWS + per - 1) / per;
-      // a CTA's only unit comes in two chunks at least, so that it is multiplied while it arrives
-      const int chunks = std::max((most + room / block - 1) / (room / block),
-                                  p.units * cluster <= 2 * sms && most >= 2 * W4S_MMA_WARPS ? 2 : 1);
+      // a CTA's only unit, where it is long, comes in two chunks at least, so that it is multiplied
+      // while it arrives (T = 1, 2112 x 2816: 36 KB in one chunk take 1.4 us longer; but T = 7 in two
+      // slices of K, 19 KB in two chunks, 0.2, and T = 16 in four, 9 blocks and their fragments, 0.5)
+      const bool halve = p.units * cluster <= 2 * sms && most >= 2 * W4S_MMA_WARPS && most * block >= 24576;
+      const int chunks = std::max((most + room / block - 1) / (room / block), halve ? 2 : 1);
       p.step = (most + chunks - 1) / chunks;
       p.stage = (p.step * block + 127) / 128 * 128;
       p.smem = w4_linear_smem<NB>(T, K, p.frag, p.stage, cluster, lg).total;
