@@ -179,16 +179,18 @@ __device__ __forceinline__ float2 w4_add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-// rint(x / s) with the correctly rounded quotient; 0 for s = 0.  Out of line: rarely needed.
+// rint(x / s) with the correctly rounded quotient; 0 unless s is positive and finite.  Out of line:
+// rarely needed.
 __device__ __noinline__ float w4_rounded_quotient(float x, float s) {
-  return s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
+  return s > 0.f && s < INFINITY ? rintf(__fdiv_rn(x, s)) : 0.f;
 }
 
 // bf16 weights w [E][K][N] (N contiguous) -> packed.  Per group, in fp32, every step one
 // rounding to nearest even: symmetric scale = bf16(max |w| / 7), code = clamp(rint(w / scale)
 // + 8, 0, 15); asymmetric lo = min(w, 0), hi = max(w, 0), scale = bf16((hi - lo) / 15), zero =
-// clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15).  A zero scale
-// gives codes and zero points of 8.
+// clamp(rint(-lo / scale), 0, 15), code = clamp(rint(w / scale) + zero, 0, 15).  A scale that is
+// zero, infinite or NaN gives codes and zero points of 8.  The extremes propagate NaN, so a group
+// with a NaN or an infinity has such a scale, whose product with 8 - 8 is NaN for all of the group.
 //
 // Bound by its instructions (11 a weight), then its bytes (2.5 to 2.6 a weight): a warp reads two
 // rows a lane, whole lines along N, straight into registers (through shared memory it took 169 us for
@@ -221,8 +223,8 @@ __global__ void __launch_bounds__(256, 5) w4_quantize_kernel(const __nv_bfloat16
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      lo = __hmin2(lo, v[i]);
-      hi = __hmax2(hi, v[i]);
+      lo = __hmin2_nan(lo, v[i]);
+      hi = __hmax2_nan(hi, v[i]);
     }
   }
   s_lo[part][pair] = lo;
@@ -231,8 +233,8 @@ __global__ void __launch_bounds__(256, 5) w4_quantize_kernel(const __nv_bfloat16
   if (in) {
     const int span = group / 16, p0 = part / span * span;   // the 16-element parts of the group
     for (int i = p0; i < p0 + span; ++i) {
-      lo = __hmin2(lo, s_lo[i][pair]);
-      hi = __hmax2(hi, s_hi[i][pair]);
+      lo = __hmin2_nan(lo, s_lo[i][pair]);
+      hi = __hmax2_nan(hi, s_hi[i][pair]);
     }
     constexpr float SNAP = 6144.f;                        // 1.5 * 2^12
     constexpr float ROUND = 12582912.f;                   // 1.5 * 2^23
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(256, 5) w4_quantize_kernel(const __nv_bfloat16
       sb[c] = __float2bfloat16_rn(ZP ? __fdiv_rn(__fsub_rn(h, l), 15.f) : __fdiv_rn(fmaxf(-l, h), 7.f));
       s[c] = __bfloat162float(sb[c]);
       inv[c] = __fdiv_rn(1.f, s[c]);
-      z[c] = ZP && s[c] > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(-l, s[c])), 0.f), 15.f) : 8;
+      z[c] = ZP && s[c] > 0.f && s[c] < INFINITY ? (int)fminf(fmaxf(rintf(__fdiv_rn(-l, s[c])), 0.f), 15.f) : 8;
       word[c][0] = word[c][1] = ((uint32_t)z[c] - BITS) * 0x11111111u;
     }
 #pragma unroll
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(256, 5) w4_quantize_kernel(const __nv_bfloat16
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int row = 2 * pair + c;
-      if (!(s[c] > 1e-30f && s[c] < 1e30f)) {   // the reciprocal or a subnormal: by division
+      if (!(s[c] > 1e-30f && s[c] < 1e30f)) {   // 0, subnormal, infinite or NaN, now or as a reciprocal: by division
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
           uint32_t exact = 0;

@@ -368,7 +368,9 @@ moe_status_t moe_w4_pack(const uint8_t *codes, const void *scales, const uint8_t
  *   symmetric:  scale = bf16(max |w| / 7);  code = clamp(rint(w / scale) + 8, 0, 15)
  *   MOE_FLAG_W4_ZEROS:  lo = min(w, 0), hi = max(w, 0);  scale = bf16((hi - lo) / 15);
  *               zero = clamp(rint(-lo / scale), 0, 15);  code = clamp(rint(w / scale) + zero, 0, 15)
- * and code = zero = 8 where scale == 0. */
+ * and code = zero = 8 where the scale is zero, infinite or NaN: a group that holds a NaN or an
+ * infinity (or, with zero points, a range hi - lo that fp32 does not hold) is NaN in every product,
+ * and no other group is touched. */
 moe_status_t moe_w4_quantize_weights(const void *w, int E, int K, int N, int group, unsigned flags,
                                      void *packed, void *stream);
 

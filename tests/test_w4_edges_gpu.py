@@ -1,4 +1,5 @@
-"""The 4-bit weight calls on the GPU where the formulas are delicate: negative gates of the GELU."""
+"""The 4-bit weight calls on the GPU where the formulas are delicate: negative gates of the GELU,
+weights that are no numbers."""
 import math
 
 import pytest
@@ -72,4 +73,47 @@ def test_gelu_far_from_zero():
     assert float(y[0].abs().max()) < 1e-30 and float(y[2].abs().max()) == 0
     want = x[1].double() ** 2
     assert bool(((y[1].double() - want).abs() <= ref.HALF_BF16 * want).all())
+    synced()
+
+
+# ----------------------------------------------------------------------------- the quantiser
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_quantise_damaged_group_is_nan(group, zeros, bad):
+    """A NaN or an infinity makes all of its group NaN, and nothing else: as the formulas have it."""
+    E, K, N = 2, 192, 80
+    g = torch.Generator().manual_seed(group)
+    w = (torch.randn((E, K, N), generator=g) * 0.02 + 0.03).to(torch.bfloat16)   # codes above 8 mostly
+    clean = moe.w4_dequantize(moe.w4_quantize(w.cuda(), group=group, zeros=zeros)).cpu()
+    assert bool(clean.isfinite().all())
+    at = [(0, 0, 0), (0, 31, 1), (1, 130, 79), (1, 191, 40), (0, 66, 16)]
+    want = clean.clone()
+    for e, k, n in at:
+        w[e, k, n] = bad
+        want[e, k // group * group:(k // group + 1) * group, n] = float("nan")
+    q = moe.w4_quantize(w.cuda(), group=group, zeros=zeros)
+    got = moe.w4_dequantize(q).cpu()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
+    # codes and zero points of such a group are 8
+    rec = q.data.cpu()[0, 0, 0]
+    assert rec[:16].tolist()[0:4] == [0x88] * 4
+    if zeros:
+        assert int(rec[512 + (64 if group == 32 else 32)]) == 8
+    synced()
+
+
+@pytest.mark.parametrize("group", [32, 128])
+def test_quantise_range_past_fp32(group):
+    """hi - lo that no fp32 holds: the scale is infinite, the group NaN."""
+    w = torch.zeros((1, 128, 16))
+    w[0, 0, 3], w[0, 1, 3] = 3e38, -3e38
+    w[0, 64, 5] = 3e38
+    q = moe.w4_quantize(w.to(torch.bfloat16).cuda(), group=group, zeros=True)
+    d = moe.w4_dequantize(q).cpu()
+    assert bool(d[0, :group, 3].isnan().all())
+    keep = torch.ones_like(d, dtype=torch.bool)
+    keep[0, :group, 3] = False
+    assert bool(d[keep].isfinite().all()) and float(d[0, 64, 5]) > 2.9e38
     synced()
