@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -472,16 +473,52 @@ def forward_nvfp4(x: torch.Tensor, w_router: torch.Tensor, wq: dict, k: int,
 
 
 # ----------------------------------------------------------------------------- 4-bit weights
+@functools.lru_cache(maxsize=256)
+def _w4_shape(E: int, K: int, N: int, group: int, zeros: bool) -> tuple[int, int, int, int]:
+    """Shape of E packed matrices [K, N] as bytes; raises for what the library does not hold."""
+    n = load().moe_w4_packed_bytes(E, K, N, group, MOE_FLAG_W4_ZEROS if zeros else 0)
+    if n == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED if group in (32, 64, 128) else MOE_ERR_INVALID_ARG,
+                       "moe_w4_packed_bytes")
+    records = E * (N // 16) * (K // 64)
+    return (E, N // 16, K // 64, n // records)
+
+
 class W4Weights:
     """E matrices [K, N] as packed 4-bit codes with group scales (and zero points): the layout of
-    include/moe.h in ``data`` (uint8 [E, N/16, K/64, R], CUDA).  Made by w4_pack or w4_quantize."""
+    include/moe.h in ``data`` (uint8 [E, N/16, K/64, R]).  Made by w4_pack or w4_quantize, or from the
+    data of an earlier one (a file, another device): W4Weights(data, E, K, N, group, zeros).  The
+    kernels trust these numbers, so they are checked against the data here and cannot be changed."""
 
     __slots__ = ("data", "E", "K", "N", "group", "zeros", "flags", "index")
 
     def __init__(self, data: torch.Tensor, E: int, K: int, N: int, group: int, zeros: bool):
-        self.data, self.E, self.K, self.N, self.group, self.zeros = data, E, K, N, group, zeros
-        self.flags = MOE_FLAG_W4_ZEROS if zeros else 0
-        self.index = data.get_device()
+        E, K, N, group = map(operator.index, (E, K, N, group))
+        zeros = bool(zeros)
+        shape = _w4_shape(E, K, N, group, zeros)
+        if not isinstance(data, torch.Tensor) or data.dtype is not torch.uint8:
+            raise TypeError("data must be a uint8 tensor")
+        if data.shape != shape:
+            raise ValueError(f"data must have shape {shape}, got {tuple(data.shape)}")
+        if not data.is_contiguous() or data.data_ptr() % 16:
+            raise ValueError("data must be contiguous and 16-byte aligned")
+        self._hold(data, E, K, N, group, zeros)
+
+    def _hold(self, data, E, K, N, group, zeros, set_=object.__setattr__):
+        set_(self, "data", data)
+        set_(self, "E", E)
+        set_(self, "K", K)
+        set_(self, "N", N)
+        set_(self, "group", group)
+        set_(self, "zeros", zeros)
+        set_(self, "flags", MOE_FLAG_W4_ZEROS if zeros else 0)
+        set_(self, "index", data.get_device())
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"W4Weights.{name} cannot be changed: make another W4Weights")
+
+    def __reduce__(self):
+        return W4Weights, (self.data, self.E, self.K, self.N, self.group, self.zeros)
 
     @property
     def shape(self) -> tuple[int, int, int]:
@@ -560,12 +597,9 @@ def _rows(x, name: str):
 
 
 def _w4_empty(E: int, K: int, N: int, group: int, zeros: bool, like) -> W4Weights:
-    n = _w4_bytes("moe_w4_packed_bytes", E, K, N, group, MOE_FLAG_W4_ZEROS if zeros else 0)
-    if n == 0:
-        raise MoEError(MOE_ERR_UNSUPPORTED if group in (32, 64, 128) else MOE_ERR_INVALID_ARG,
-                       "moe_w4_packed_bytes")
-    data = like.new_empty((E, N // 16, K // 64, n // (E * (N // 16) * (K // 64))), dtype=_U8)
-    return W4Weights(data, E, K, N, group, zeros)
+    w = W4Weights.__new__(W4Weights)
+    w._hold(like.new_empty(_w4_shape(E, K, N, group, zeros), dtype=_U8), E, K, N, group, zeros)
+    return w
 
 
 def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
@@ -616,7 +650,7 @@ def w4_quantize(w: torch.Tensor, group: int = 64, zeros: bool = False, stream=No
 def w4_dequantize(w: W4Weights, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """moe_w4_dequantize_weights: the bf16 weights [E, K, N] that w stands for (what forward and
     dense_ffn take for larger batches)."""
-    if type(w) is not W4Weights:
+    if type(w) is not W4Weights or w.index < 0:
         raise TypeError("w must be W4Weights on a CUDA device (w4_pack, w4_quantize)")
     if stream is not None or w.index != _current_device():
         return _elsewhere(w4_dequantize, w, stream, (w, out))
