@@ -784,9 +784,10 @@ def forward_w4(x: torch.Tensor, w_router: torch.Tensor, w_gate: W4Weights, w_up:
 
 
 def _aux_out(T: int, E: int, k: int, dev) -> tuple[AuxOut, dict]:
+    new = torch.empty if T else torch.zeros   # without tokens nothing is launched
     aux_d = {
-        "expert_counts": torch.empty(E, dtype=torch.int32, device=dev),
-        "expert_offsets": torch.empty(E + 1, dtype=torch.int32, device=dev),
+        "expert_counts": new(E, dtype=torch.int32, device=dev),
+        "expert_offsets": new(E + 1, dtype=torch.int32, device=dev),
         "perm": torch.empty(T * k, dtype=torch.int32, device=dev),
         "topk_ids": torch.empty((T, k), dtype=torch.int32, device=dev),
         "topk_weights": torch.empty((T, k), dtype=torch.float32, device=dev),

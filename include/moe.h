@@ -402,7 +402,8 @@ moe_status_t moe_dense_ffn_w4(const void *x, const void *w_gate, const void *w_u
  * is taken in fp32 of the fp64 logits' differences), experts as moe_forward: w_gate, w_up E packed
  * matrices (K = H, N = I), w_down E packed matrices (K = I, N = H).  h is rounded to bf16; the
  * expert outputs and their weighted sum stay in fp32 until y.  flags:
- * MOE_FLAG_NO_RENORM, MOE_FLAG_W4_ZEROS.  aux as moe_forward.  Shapes as moe_forward, T <= 16.
+ * MOE_FLAG_NO_RENORM, MOE_FLAG_W4_ZEROS.  aux as moe_forward (T == 0 writes nothing, aux neither).
+ * Shapes as moe_forward, T <= 16.
  * Workspace: moe_w4_workspace_size bytes (0 = unsupported shape).
  */
 size_t moe_w4_workspace_size(int T, int H, int E, int I, int k, unsigned flags);

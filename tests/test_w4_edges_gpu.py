@@ -1,5 +1,5 @@
 """The 4-bit weight calls on the GPU where the formulas are delicate: negative gates of the GELU,
-weights that are no numbers."""
+weights that are no numbers, batches without tokens."""
 import math
 
 import pytest
@@ -117,3 +117,18 @@ def test_quantise_range_past_fp32(group):
     keep[0, :group, 3] = False
     assert bool(d[keep].isfinite().all()) and float(d[0, 64, 5]) > 2.9e38
     synced()
+
+
+# ----------------------------------------------------------------------------- no tokens
+def test_layer_without_tokens_counts_none():
+    """Empty batches: counts and offsets are zeros, whatever the memory held."""
+    E = 16
+    m = identity(E, 64)
+    wr = torch.zeros((64, E), dtype=torch.bfloat16, device="cuda")
+    used = [torch.full((n,), 7, dtype=torch.int32, device="cuda") for n in (E, E + 1, 5) * 4]
+    del used
+    y, aux = moe.forward_w4(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), wr, m, m, m, 2, aux=True)
+    assert y.shape == (0, 64) and aux["topk_weights"].shape == (0, 2) and aux["perm"].shape == (0,)
+    assert aux["expert_counts"].tolist() == [0] * E
+    assert aux["expert_offsets"].tolist() == [0] * (E + 1)
+    assert aux["router_stats"].tolist() == [0] * 5
