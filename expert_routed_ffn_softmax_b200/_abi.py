@@ -98,6 +98,7 @@ SIGNATURES = {
     "moe_cuda_error_name": (ctypes.c_char_p, [_I]),
     "moe_debug_set_wait_limit_ns": (_I, [ctypes.c_ulonglong]),
     "moe_debug_unsatisfied_wait": (_I, [_P]),
+    "moe_debug_w4_cut": (_I, [_I, _I, _I, _I, _U, _I, _I, ctypes.POINTER(_I)]),
 }
 
 

@@ -45,7 +45,7 @@ int w4_slots(const DeviceState& d) { return 2 * std::max(1, d.num_sms); }
 // 704 to 131072) and all 16 cuts of each, timed one by one, the choice was within 8 % of the best
 // (18 % at T = 12, 16384 x 2048).
 struct W4Plan {
-  int lg = 0, cluster = 1, units = 0, step = 0, stage = 0, smem = 0, frag = 0;
+  int lg = 0, cluster = 1, units = 0, step = 0, stage = 0, smem = 0, frag = 0, steal = 0;
 };
 // Whether activations [T][K] come as fragments.
 template <int NB> bool w4_frag(int T, int K) {
@@ -91,6 +91,7 @@ W4Plan w4_plan(int mode, int T, int K, int N, int record, int sms) {
         best = p;
       }
     }
+  best.steal = best.cluster == 1 && best.units > 2 * sms;
   return best;
 }
 
@@ -106,7 +107,7 @@ moe_status_t w4_stream(cudaStream_t st, const DeviceState& d, W4Linear a, int gr
     a.step = p.step;
     a.stage = p.stage;
     a.frag = p.frag;
-    a.steal = p.cluster == 1 && p.units > 2 * sms;
+    a.steal = p.steal;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.units * p.cluster);
     cfg.blockDim = dim3(W4S_THREADS);
@@ -435,6 +436,16 @@ moe_status_t moe_forward_w4(const void* x, const void* w_router, const float* ro
            dim3(W4S_THREADS), W4S_SMEM, a);
   });
   return launched();
+}
+
+moe_status_t moe_debug_w4_cut(int T, int K, int N, int group, unsigned flags, int geglu, int sms, int* out) {
+  if (!out || !w4_group_ok(group) || (flags & ~MOE_FLAG_W4_ZEROS) || sms < 1) return MOE_ERR_INVALID_ARG;
+  if (T < 1 || T > W4_MAX_T || !w4_matrix_ok(K, N)) return MOE_ERR_UNSUPPORTED;
+  const int mode = geglu ? W4_GEGLU : W4_LINEAR, record = w4_record(group, flags & MOE_FLAG_W4_ZEROS);
+  const W4Plan p = T > 8 ? w4_plan<2>(mode, T, K, N, record, sms) : w4_plan<1>(mode, T, K, N, record, sms);
+  const int cut[6] = {p.cluster, 2 << p.lg, p.units, p.step, p.frag, p.steal};
+  std::copy(cut, cut + 6, out);
+  return MOE_OK;
 }
 
 }  // extern "C"

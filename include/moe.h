@@ -476,6 +476,13 @@ const char *moe_stage_name(int i);
 moe_status_t moe_debug_set_wait_limit_ns(unsigned long long ns);
 moe_status_t moe_debug_unsatisfied_wait(void *stream);
 
+/* Testing aid for the 4-bit products: how moe_linear_w4 (or, with geglu, the gate | up half of
+ * moe_dense_ffn_w4: N = I) cuts this shape on a device of `sms` SMs.  Host only.  cut[0..5]: CTAs
+ * that share a unit's K, 16-row strips of a unit, units, 64-element blocks of a chunk, 1 if the
+ * activations come as fragments, 1 if CTAs take over units of CTAs that have not started. */
+moe_status_t moe_debug_w4_cut(int T, int K, int N, int group, unsigned flags, int geglu, int sms,
+                              int *cut);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,13 +1,17 @@
-"""4-bit weights without a GPU: an object that names packed weights holds them."""
+"""4-bit weights without a GPU: an object that names packed weights holds them, and the ways of
+cutting a product are the ones that the GPU tests run."""
 import copy
+import ctypes
 import io
 import pickle
+import random
 
 import pytest
 import torch
 
 import expert_routed_ffn_softmax_b200 as moe
 from expert_routed_ffn_softmax_b200 import _abi, build
+from w4_cuts import CUTS
 
 
 @pytest.fixture(scope="module")
@@ -80,3 +84,42 @@ def test_weights_object_through_files_and_copies(lib):
 def test_weights_on_the_host_are_refused_by_the_calls(lib):
     with pytest.raises(TypeError, match="CUDA"):
         moe.w4_dequantize(moe.W4Weights(packed(), 2, 128, 32, 64, False))
+
+
+# ----------------------------------------------------------------------------- cuts
+def cut_of(lib, geglu, T, K, N, group, zeros, sms=148):
+    cut = (ctypes.c_int * 6)()
+    rc = lib.moe_debug_w4_cut(T, K, N, group, _abi.MOE_FLAG_W4_ZEROS if zeros else 0, geglu, sms, cut)
+    assert rc == 0
+    cluster, strips, units, step, frag, steal = cut
+    # every strip is in a unit and every block in a chunk, with nothing left over
+    per = strips // 2 if geglu else strips
+    assert (units - 1) * per < N // 16 <= units * per and cluster <= K // 64
+    assert 1 <= step <= -(-(K // 64) // cluster)
+    return geglu, cluster, strips, frag, steal
+
+
+def test_listed_cuts_are_the_ones_taken(lib):
+    for row in CUTS:
+        assert cut_of(lib, row[0], *row[5:]) == row[:5], row
+    assert len({row[:5] for row in CUTS}) == len(CUTS)
+
+
+def test_no_cut_is_taken_that_is_not_listed(lib):
+    rng, listed = random.Random(3), {row[:5] for row in CUTS}
+    for _ in range(20000):
+        geglu = rng.random() < 0.4
+        N = 64 * int(2 ** rng.uniform(0, 7)) if geglu else 16 * int(2 ** rng.uniform(0, 16))
+        shape = (rng.randint(1, 16), 64 * int(2 ** rng.uniform(0, 8)), N, rng.choice((32, 64, 128)),
+                 rng.random() < 0.5)
+        assert cut_of(lib, int(geglu), *shape) in listed, shape
+
+
+def test_cut_query_refuses(lib):
+    f, out = lib.moe_debug_w4_cut, (ctypes.c_int * 6)()
+    assert f(8, 128, 64, 64, 0, 0, 148, None) == _abi.MOE_ERR_INVALID_ARG
+    assert f(8, 128, 64, 48, 0, 0, 148, out) == _abi.MOE_ERR_INVALID_ARG
+    assert f(8, 128, 64, 64, 1, 0, 148, out) == _abi.MOE_ERR_INVALID_ARG
+    assert f(8, 128, 64, 64, 0, 0, 0, out) == _abi.MOE_ERR_INVALID_ARG
+    for bad in ((0, 128, 64), (17, 128, 64), (8, 100, 64), (8, 128, 24)):
+        assert f(*bad, 64, 0, 0, 148, out) == _abi.MOE_ERR_UNSUPPORTED
