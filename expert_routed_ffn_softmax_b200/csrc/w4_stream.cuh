@@ -59,7 +59,7 @@ __device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity, const vo
         : "r"(bar), "r"(parity), "r"(kParkNs)
         : "memory");
     if (ok) return true;
-    if (abort && *abort) return false;
+    if (*abort) return false;
     const uint64_t now = global_timer_ns();
     if (t0 == 0) t0 = now;
     if (now - t0 > *reinterpret_cast<volatile unsigned long long*>(&g_wait_limit_ns)) {
@@ -72,7 +72,7 @@ __device__ __forceinline__ bool w4s_wait(uint32_t bar, uint32_t parity, const vo
 // Barriers and flags of a CTA.
 struct W4Sync {
   uint32_t base;
-  volatile int* flags;   // {abort, phases issued (chunks, the end), activations issued}
+  volatile int* flags;   // {abort, phases issued (chunks, the end), activations issued, takeovers asked for}
   __device__ uint32_t full(int s) const { return base + 8u * s; }
   __device__ uint32_t empty(int s) const { return base + 8u * (W4S_STAGES + s); }
   __device__ uint32_t acc_full(int b) const { return base + 8u * (2 * W4S_STAGES + b); }
@@ -96,18 +96,21 @@ struct W4Sync {
     }
     mbar_init(act_full(), 1);
     mbar_init(steal_full(), 1);
-    flags[0] = flags[1] = flags[2] = 0;
+    flags[0] = flags[1] = flags[2] = flags[3] = 0;
     fence_barrier_init();
   }
   __device__ void abort() const { flags[0] = 1; }
   __device__ bool aborted() const { return flags[0] != 0; }
   __device__ bool wait(uint32_t bar, uint32_t parity) const { return w4s_wait(bar, parity, flags); }
-  // After the roles have ended with an abort: wait for the copies of the last chunks (a stage is
-  // issued again only when its chunk has been consumed).
+  // After the roles have ended with an abort: wait for everything that still writes this CTA's shared
+  // memory, whatever the limit of the other waits: the copies of the last chunks (a stage is issued
+  // again only when its chunk has been consumed), the activations, the answer to the last request to
+  // take over a unit (the next request is made only when the answer before it has been read).
   __device__ void drain() const {
     for (int q = max(0, flags[1] - W4S_STAGES); q < flags[1]; ++q)
       mbar_wait_ns(full(q % W4S_STAGES), (q / W4S_STAGES) & 1, kDrainLimitNs);
     if (flags[2]) mbar_wait_ns(act_full(), 0, kDrainLimitNs);
+    if (flags[3]) mbar_wait_ns(steal_full(), (flags[3] - 1) & 1, kDrainLimitNs);
   }
 };
 
@@ -338,7 +341,10 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
       if (ok && waited) activations(0);
       for (int u = first_unit; u >= 0 && ok; ++n_unit) {
         unit_ring[n_unit % W4S_UNITS] = u;
-        if (a.steal) steal_request(answer, sy.steal_full());
+        if (a.steal) {
+          sy.flags[3] = ++n_steal;
+          steal_request(answer, sy.steal_full());
+        }
         const int ns = strips_of(u), all = MODE == W4_GEGLU ? 2 * ns : ns;
         const size_t at = ((size_t)u << (MODE == W4_GEGLU ? a.lg : a.lg + 1)) * pitch + (size_t)k0 * R;
         for (int b = 0; b < blocks; b += a.step, ++q, pos.next()) {
@@ -368,10 +374,8 @@ __global__ void __launch_bounds__(W4S_THREADS, 2) w4_linear_kernel(const __grid_
         if (!waited) wait_previous(q);
         u = -1;
         if (a.steal) {
-          // also when giving up: the answer must not arrive in a CTA that has ended
-          if (!w4s_wait(sy.steal_full(), n_steal & 1, nullptr)) ok = false;
+          if (!sy.wait(sy.steal_full(), (n_steal - 1) & 1)) ok = false;
           else u = steal_answer(answer);
-          ++n_steal;
         }
       }
       if (!waited) pdl_wait();

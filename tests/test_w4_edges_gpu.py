@@ -1,5 +1,6 @@
 """The 4-bit weight calls on the GPU where the formulas are delicate: negative gates of the GELU,
-weights that are no numbers, batches without tokens."""
+weights that are no numbers, batches without tokens, waits that run out."""
+import ctypes
 import math
 
 import pytest
@@ -7,12 +8,22 @@ import torch
 
 import expert_routed_ffn_softmax_b200 as moe
 import w4_reference as ref
+from expert_routed_ffn_softmax_b200 import _abi
 
 pytestmark = pytest.mark.gpu
 
 
 def synced():
     assert moe.sync_status() == 0
+
+
+def cut_of(T, K, N, geglu):
+    """{CTAs of a unit's K, strips, units, blocks a chunk, fragments, take-over} of a product of group 32
+    with zero points."""
+    cut = (ctypes.c_int * 6)()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert moe.load().moe_debug_w4_cut(T, K, N, 32, _abi.MOE_FLAG_W4_ZEROS, geglu, sms, cut) == 0
+    return list(cut)
 
 
 # ----------------------------------------------------------------------------- GELU
@@ -132,3 +143,50 @@ def test_layer_without_tokens_counts_none():
     assert aux["expert_counts"].tolist() == [0] * E
     assert aux["expert_offsets"].tolist() == [0] * (E + 1)
     assert aux["router_stats"].tolist() == [0] * 5
+
+
+# ----------------------------------------------------------------------------- waits that run out
+def random_weights(K, N, seed):
+    """Random codes of group 32 under one scale and zero point, made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    return moe.w4_pack(codes, torch.full((N, K // 32), 0.01, dtype=torch.bfloat16, device="cuda"),
+                       torch.full((N, K // 32), 7, dtype=torch.uint8, device="cuda"), group=32)
+
+
+def gives_up(call):
+    """With the wait limit at next to nothing the call's waits run out: it returns, the error is
+    reported once, and the next calls are right again."""
+    want = call()
+    synced()
+    lib = moe.load()
+    for _ in range(3):
+        assert lib.moe_debug_set_wait_limit_ns(1) == 0
+        try:
+            call()
+            status = moe.sync_status()
+        finally:
+            assert lib.moe_debug_set_wait_limit_ns(0) == 0
+        assert status == _abi.MOE_ERR_TIMEOUT
+        synced()
+        assert torch.equal(call(), want)
+    synced()
+
+
+def test_linear_gives_up_while_units_are_taken_over():
+    """A unit of 128 rows over K = 16384 takes some 90 us, during which the joining warps wait; each CTA
+    has asked for its next unit by then."""
+    T, K, N = 16, 16384, 131072
+    assert cut_of(T, K, N, 0)[1::4] == [8, 1]
+    w = random_weights(K, N, 1)
+    x = torch.randn((T, K), device="cuda").to(torch.bfloat16)
+    gives_up(lambda: moe.linear_w4(x, w))
+
+
+def test_dense_gives_up_in_clusters_that_started_early():
+    """The second product's first clusters start while the first product runs, and wait for its h."""
+    T, H, I = 16, 16384, 5760
+    assert cut_of(T, I, H, 0)[0] == 2 and cut_of(T, H, I, 1)[0] == 2
+    g, u, d = random_weights(H, I, 1), random_weights(H, I, 2), random_weights(I, H, 3)
+    x = torch.randn((T, H), device="cuda").to(torch.bfloat16)
+    gives_up(lambda: moe.dense_ffn_w4(x, g, u, d))
