@@ -32,18 +32,20 @@ int w4_slots(const DeviceState& d) { return 2 * std::max(1, d.num_sms); }
 
 // How a linear layer (or the gate | up half of a GEGLU MLP) is cut: units of 2 << lg strips,
 // `cluster` CTAs sharing a unit's K.  A CTA keeps its slice of the activations in shared memory
-// where they fit beside the ring (rows up to T K = 22 K elements, say); longer ones come as
-// fragments with each chunk of weights.  A taller unit reads the activations less often, a lower one
-// and slices of K spread a small matrix over the SMs (two CTAs each).  More units than run at once
-// are only stolen without clusters: a cluster's start and meeting would be paid for every unit.
+// where all of K would fit beside a ring of two 16 KB stages (T <= 8, rows up to T K = 30 K elements);
+// longer ones come as fragments with each chunk of weights.  A taller unit reads the activations less
+// often, a lower one and slices of K spread a small matrix over the SMs (two CTAs each).  More units
+// than run at once are only stolen without clusters: a cluster's start and meeting would be paid for
+// every unit.
 //
 // The choice is the one with the least time by a model of what was measured on B200 (ns).  Per
 // block and strip, the largest of: decoding and products, 26 with two CTAs on an SM and 18 + 1.1 T
 // with one (45 for two row tiles); its bytes at 22 a ns (32 for a CTA alone on its SM, without
 // fragments); its copies at 100 each.  Per cluster 400 a CTA (200 with fragments, whose own launch
-// hides its start) and 0.3 for every sum exchanged.  Over 17 shapes (T 1 to 16, K 704 to 16384, N
-// 704 to 131072) and all 16 cuts of each, timed one by one, the choice was within 8 % of the best
-// (18 % at T = 12, 16384 x 2048).
+// hides its start) and 0.3 for every sum exchanged.  The model ranks cuts; what every cut pays alike
+// (launches, the first copy, the last join: 3 to 6 us) is not in it.  Over 17 shapes (T 1 to 16, K 704
+// to 16384, N 704 to 131072) and all 16 cuts of each, timed one by one, the choice was within 7 % of
+// the best (10 % at T = 12, 16384 x 2048) and the best itself in 9 of them.
 struct W4Plan {
   int lg = 0, cluster = 1, units = 0, step = 0, stage = 0, smem = 0, frag = 0, steal = 0;
 };
@@ -103,7 +105,6 @@ moe_status_t w4_stream(cudaStream_t st, const DeviceState& d, W4Linear a, int gr
     const W4Plan p = w4_plan<NB>(MODE, a.T, a.K, a.N, w4_record(group, zeros), sms);
     a.lg = p.lg;
     a.cluster = p.cluster;
-    a.units = p.units;
     a.step = p.step;
     a.stage = p.stage;
     a.frag = p.frag;

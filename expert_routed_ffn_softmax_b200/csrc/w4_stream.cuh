@@ -241,7 +241,7 @@ struct W4Linear {
   void* out;                    // [T][N]
   int T, K, N;
   int lg;                       // log2 of the row groups: 2 << lg strips per unit
-  int units, step;              // blocks per chunk
+  int step;                     // blocks per chunk
   int stage;                    // bytes of a stage
   int frag;                     // 1: act holds fragments and a chunk brings its blocks' along;
                                 // 0: a CTA keeps all of act in shared memory
