@@ -185,3 +185,136 @@ def test_layer_weights_are_within_1e6_of_route(T, H, E, k, spread, bias, renorm)
     exact = oracle.route(x.cpu(), wr.cpu(), k, bias=None if b is None else b.cpu(), renorm=renorm)[1]
     assert np.abs(aux["topk_weights"].cpu().numpy().astype(np.float64) - exact).max() <= 1e-6
     synced()
+
+
+# ----------------------------------------------------------------------------- the limits
+def test_linear_at_the_limits():
+    for T, K, N in ((16, 64, 1048576), (1, 64, 1048576), (16, 16384, 16), (1, 16384, 16)):
+        w, v = gpu_matrix(K, N, 64, True, 7)
+        x = rows(T, K, 1)
+        y, err = ref.linear(x, v[0], 64)
+        check(moe.linear_w4(x, w, fp32=True), y, err)
+    synced()
+
+
+def test_dense_at_the_limits():
+    T, H, I = 16, 16384, 8192
+    m = [gpu_matrix(*s, 32, True, i) for i, s in enumerate(((H, I), (H, I), (I, H)))]
+    x = (rows(T, H, 1).float() * 0.1).to(torch.bfloat16)
+    y, err = ref.ffn(x, *[v[0] for _, v in m], 32)
+    check(moe.dense_ffn_w4(x, *[w for w, _ in m]), y, err)
+    synced()
+
+
+def test_layer_at_the_limits():
+    """The widest layer: every token on both of its experts' 134 M weights a projection."""
+    T, H, I, E, k = 16, 16384, 8192, 4, 2
+    m = [gpu_matrix(*s, 64, False, i, E) for i, s in enumerate(((H, I), (H, I), (I, H)))]
+    x = (rows(T, H, 1).float() * 0.1).to(torch.bfloat16)
+    wr = rows(H, E, 2)
+    y, aux = moe.forward_w4(x, wr, *[w for w, _ in m], k, aux=True)
+    ids, wts = moe.route(x, wr, k)
+    assert torch.equal(aux["topk_ids"], ids)
+    want = torch.zeros((T, H), dtype=torch.float64, device="cuda")
+    err = torch.zeros_like(want)
+    for e in range(E):
+        o, eo = ref.ffn(x, *[v[e] for _, v in m], 64)
+        w = (wts * (ids == e)).sum(1, keepdim=True).double()
+        want += w * o
+        err += w * eo + 1e-6 * (o.abs() + eo) + 4 * ref.U32 * w * o.abs()
+    check(y, want, err)
+    synced()
+
+
+def test_many_small_matrices():
+    """4096 matrices of one record a strip: pack, quantise and back."""
+    E, K, N = 4096, 64, 16
+    codes = torch.randint(0, 256, (E, N, K // 2), device="cuda", dtype=torch.uint8)
+    scales = torch.rand((E, N, 1), device="cuda").to(torch.bfloat16)
+    d = moe.w4_dequantize(moe.w4_pack(codes, scales, group=64))
+    c = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).double()
+    assert torch.equal(d, ((c - 8) * scales.double()).transpose(1, 2).to(torch.bfloat16))
+    q = moe.w4_quantize(d, group=64, zeros=True)
+    assert torch.equal(q.data[4095], moe.w4_quantize(d[4095], group=64, zeros=True).data[0])
+    synced()
+
+
+# ----------------------------------------------------------------------------- odd values and places
+def small_layer(T, k=3, seed=0):
+    H, I, E = 256, 128, 16
+    q = [gpu_matrix(*s, 64, True, seed + i, E)[0] for i, s in enumerate(((H, I), (H, I), (I, H)))]
+    return rows(T, H, seed), rows(H, E, seed + 9), q, k
+
+
+@pytest.mark.parametrize("T", [2, 7, 9, 16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_rows_that_are_no_numbers_stay_apart(T, bad):
+    """A damaged token reaches neither the other tokens of the layer and the dense MLP nor an id out of
+    range; the call's status stays OK."""
+    x, wr, q, k = small_layer(T)
+    d = [gpu_matrix(*s, 64, True, 30 + i)[0] for i, s in enumerate(((256, 192), (256, 192), (192, 256)))]
+    clean, dense = moe.forward_w4(x, wr, *q, k), moe.dense_ffn_w4(x, *d)
+    x2 = x.clone()
+    x2[T // 2, 5] = bad
+    y, aux = moe.forward_w4(x2, wr, *q, k, aux=True)
+    z = moe.dense_ffn_w4(x2, *d)
+    keep = torch.arange(T) != T // 2
+    ids = aux["topk_ids"]
+    assert bool(((ids >= 0) & (ids < 16)).all()) and int(aux["expert_counts"].sum()) == T * k
+    ids2, _ = moe.route(x2, wr, k)
+    assert torch.equal(ids, ids2)
+    # units of the same height: a token's sums are in the same order, whoever shares its experts
+    assert torch.equal(y[keep], clean[keep]) and torch.equal(z[keep], dense[keep])
+    assert bool(y[T // 2].isnan().any()) and bool(z[T // 2].isnan().any())
+    synced()
+
+
+def test_bias_that_masks_experts():
+    """Experts at the lowest fp32 value or at -infinity are not chosen while others are left."""
+    x, wr, q, k = small_layer(8)
+    for low in (torch.finfo(torch.float32).min, float("-inf")):
+        b = torch.zeros(16, device="cuda")
+        b[2::2] = low
+        b[1] = low
+        y, aux = moe.forward_w4(x, wr, *q, k, bias=b, aux=True)
+        ids, w = moe.route(x, wr, k, bias=b)
+        assert torch.equal(aux["topk_ids"], ids) and bool((b[ids.long()] == 0).all())
+        assert float((aux["topk_weights"] - w).abs().max()) <= 1e-6
+        assert bool(y.isfinite().all())
+    synced()
+
+
+def test_activations_below_the_normal_range():
+    """Subnormal bf16 activations count."""
+    w, v = gpu_matrix(256, 64, 64, False, 3)
+    x = (rows(9, 256, 1).double() * 2.0 ** -129).to(torch.bfloat16)
+    assert 0 < float(x.abs().max()) < 2.0 ** -125
+    big = moe.W4Weights(w.data.clone(), 1, 256, 64, 64, False)
+    big.data[..., 512:] = torch.tensor([0x80, 0x5F], dtype=torch.uint8, device="cuda").repeat(16)   # 2^64
+    c = moe.w4_dequantize(big).double()
+    y, err = ref.linear(x, c[0], 64)
+    check(moe.linear_w4(x, big, fp32=True), y, err)
+    synced()
+
+
+def test_rows_around_the_outputs_stay():
+    """out= in the middle of a buffer: the layer and the dense MLP write their rows only."""
+    x, wr, q, k = small_layer(5)
+    d = [gpu_matrix(*s, 64, True, 30 + i)[0] for i, s in enumerate(((256, 192), (256, 192), (192, 256)))]
+    for call in (lambda o: moe.forward_w4(x, wr, *q, k, out=o), lambda o: moe.dense_ffn_w4(x, *d, out=o)):
+        buf = torch.full((12, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+        want = call(None)
+        assert call(buf[4:9]).data_ptr() == buf[4:9].data_ptr()
+        assert torch.equal(buf[4:9], want) and bool((buf[:4] == 7).all()) and bool((buf[9:] == 7).all())
+    synced()
+
+
+def test_layer_with_outputs_on_another_stream():
+    x, wr, q, k = small_layer(6)
+    want, aux = moe.forward_w4(x, wr, *q, k, aux=True)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got, aux2 = moe.forward_w4(x, wr, *q, k, aux=True, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want) and all(torch.equal(aux[n], aux2[n]) for n in aux)
+    synced()
