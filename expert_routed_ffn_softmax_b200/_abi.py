@@ -612,6 +612,8 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | Non
         raise TypeError("codes must be a CUDA tensor")
     if stream is not None or not _here(codes):
         return _elsewhere(w4_pack, codes, stream, (codes, scales, zeros, group))
+    if not isinstance(scales, torch.Tensor) or not (zeros is None or isinstance(zeros, torch.Tensor)):
+        raise TypeError("scales must be a CUDA tensor, zeros too or None")
     if codes.dim() == 2:
         codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
         zeros = None if zeros is None else zeros.unsqueeze(0)
@@ -649,8 +651,8 @@ def w4_quantize(w: torch.Tensor, group: int = 64, zeros: bool = False, stream=No
 
 
 def w4_dequantize(w: W4Weights, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """moe_w4_dequantize_weights: the bf16 weights [E, K, N] that w stands for (what forward and
-    dense_ffn take for larger batches)."""
+    """moe_w4_dequantize_weights: the bf16 weights [E, K, N] that w stands for: what forward takes for
+    larger batches, and [0] of it what dense_ffn takes."""
     if type(w) is not W4Weights or w.index < 0:
         raise TypeError("w must be W4Weights on a CUDA device (w4_pack, w4_quantize)")
     if stream is not None or w.index != _current_device():

@@ -190,3 +190,27 @@ def test_dense_gives_up_in_clusters_that_started_early():
     g, u, d = random_weights(H, I, 1), random_weights(H, I, 2), random_weights(I, H, 3)
     x = torch.randn((T, H), device="cuda").to(torch.bfloat16)
     gives_up(lambda: moe.dense_ffn_w4(x, g, u, d))
+
+
+# ----------------------------------------------------------------------------- the binding
+def test_dense_ffn_takes_dequantised_matrices():
+    """The documented way to larger batches: one matrix of w4_dequantize is what dense_ffn takes.  The
+    two round alike (h and y to bf16), but for sums in another order and dense_ffn's weights, each
+    rounded once: three half steps."""
+    H, I = 256, 192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = [moe.w4_quantize((torch.randn(s, generator=g, device="cuda") * 0.05).to(torch.bfloat16), zeros=True)
+         for s in ((H, I), (H, I), (I, H))]
+    x = torch.randn((64, H), generator=g, device="cuda").to(torch.bfloat16)
+    y = moe.dense_ffn(x, *[moe.w4_dequantize(m)[0] for m in q]).double()
+    z = torch.cat([moe.dense_ffn_w4(x[i:i + 16], *q) for i in range(0, 64, 16)]).double()
+    assert float((y - z).norm() / z.norm()) < 3 * ref.HALF_BF16
+    synced()
+
+
+def test_pack_refuses_what_is_no_tensor():
+    c = torch.zeros((32, 64), dtype=torch.uint8, device="cuda")
+    s = torch.ones((32, 2), dtype=torch.bfloat16, device="cuda")
+    for bad in ((c, None, None), (c, 1.0, None), (c, s, 8), (c.unsqueeze(0), s.unsqueeze(0), [8])):
+        with pytest.raises(TypeError):
+            moe.w4_pack(*bad)
