@@ -271,8 +271,9 @@ __device__ __forceinline__ void w4_select(const W4Moe& a, int t, uint8_t* scratc
       // the ids at once: other CTAs poll them to start their streams; the weights are needed last
       if (lane < a.k) *reinterpret_cast<volatile int32_t*>(a.ids + (size_t)t * a.k + lane) = sSelE[lane];
       // The differences are taken in fp64; their exponentials and the sum in fp32 (the weights are
-      // fp32: off by 2^-24 |difference| plus a few 2^-24).  The fp64 exp's code alone, fetched
-      // cold once a launch, took 3 us.
+      // fp32: off by at most 0.37 * 2^-24 for the differences' rounding plus a few 2^-24; a token that
+      // goes through w4_exact_token gets them in fp64, within the same 1e-6).  The fp64 exp's code
+      // alone, fetched cold once a launch, took 3 us.
       const double m = sSelV[0];
       const float ex = lane < a.k ? expf((float)(sSelV[lane] - m)) : 0.f;
       float sum = ex;
