@@ -521,6 +521,11 @@ class W4Weights:
     def __reduce__(self):
         return W4Weights, (self.data, self.E, self.K, self.N, self.group, self.zeros)
 
+    def __setstate__(self, state):
+        """Objects saved with their attributes as state, as plain slots are."""
+        was = state[1]
+        self.__init__(*(was[n] for n in ("data", "E", "K", "N", "group", "zeros")))
+
     @property
     def shape(self) -> tuple[int, int, int]:
         return (self.E, self.K, self.N)

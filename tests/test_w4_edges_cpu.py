@@ -81,6 +81,17 @@ def test_weights_object_through_files_and_copies(lib):
         fn(args[0][:1], *args[1:])
 
 
+def test_weights_object_saved_as_plain_slots(lib):
+    """The state that a pickle of plain slots holds; a device number in it is not believed."""
+    w = moe.W4Weights(packed(), 2, 128, 32, 64, False)
+    slots = {n: getattr(w, n) for n in ("data", "E", "K", "N", "group", "zeros", "flags")}
+    c = moe.W4Weights.__new__(moe.W4Weights)
+    c.__setstate__((None, {**slots, "index": 3}))
+    assert c.shape == w.shape and c.index == -1 and c.data is w.data
+    with pytest.raises(ValueError):
+        moe.W4Weights.__new__(moe.W4Weights).__setstate__((None, {**slots, "group": 32, "index": 0}))
+
+
 def test_weights_on_the_host_are_refused_by_the_calls(lib):
     with pytest.raises(TypeError, match="CUDA"):
         moe.w4_dequantize(moe.W4Weights(packed(), 2, 128, 32, 64, False))
